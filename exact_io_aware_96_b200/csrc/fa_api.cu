@@ -734,3 +734,6 @@ int fa_last_device_status(int* detail) {
 }
 
 }  // extern "C"
+
+// Differential attention and rotary positions.
+#include "fa_api_diff.cuh"

@@ -1,0 +1,343 @@
+// fa_api_diff.cuh — the C ABI of differential attention and of the rotary
+// positions (include/fa.h): argument checks, tensor maps, workspace layout,
+// launches. Part of fa_api.cu's translation unit, whose helpers it uses. No
+// allocation, no host synchronisation, nothing that throws.
+#pragma once
+
+#include "fa_diff_bwd.cuh"
+#include "fa_diff_fwd.cuh"
+#include "fa_rotary.cuh"
+
+namespace {
+
+void set_strides(int64_t (&s)[3], const fa_tensor& t) {
+  s[0] = t.stride_b;
+  s[1] = t.stride_s;
+  s[2] = t.stride_h;
+}
+
+// Axes of extent > 1 must be stepped over: a zero stride there (an expanded
+// view) is refused, for inputs because a tensor map cannot hold it and for
+// outputs because rows would overwrite one another.
+int check_axes(const fa_tensor& t, int B, int S, int H) {
+  if ((B > 1 && t.stride_b == 0) || (S > 1 && t.stride_s == 0) || (H > 1 && t.stride_h == 0))
+    return FA_ERR_INVALID_ARG;
+  // A tensor map holds byte strides below 2^40.
+  const int64_t lim = int64_t(1) << 39;
+  if (t.stride_b >= lim || t.stride_s >= lim || t.stride_h >= lim) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int check_diff(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, float scale, int causal, int dtype) {
+  int st = check_common(B, H, Sq, Sk, D, scale, causal, dtype);
+  if (st != FA_OK) return st;
+  if (D > 64 || Dv < 8 || Dv > 128 || Dv % 8) return FA_ERR_UNSUPPORTED;
+  if (Hk < 1 || H % Hk) return FA_ERR_INVALID_ARG;
+  // Row indices of both maps' fp32 dQ accumulators are 32-bit tensor-map
+  // coordinates, and grids are 31-bit.
+  const int64_t lim = (int64_t(1) << 31) - 1;
+  if (2 * int64_t(B) * H * ((int64_t(Sq) + 127) / 128 * 128) > lim) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int check_lam(const fa_diff_lambda& l, int B, int Sq, int H, int dtype) {
+  if (l.ptr == nullptr) return FA_ERR_INVALID_ARG;
+  if (l.dtype != FA_LAMBDA_FP32 && l.dtype != dtype) return FA_ERR_UNSUPPORTED;
+  if (l.stride_b < 0 || l.stride_s < 0 || l.stride_h < 0) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(l.ptr) & (l.dtype == FA_LAMBDA_FP32 ? 3u : 1u)) return FA_ERR_MISALIGNED;
+  if ((l.extent_b != 1 && l.extent_b != B) || (l.extent_s != 1 && l.extent_s != Sq) ||
+      (l.extent_h != 1 && l.extent_h != H))
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int lam_kind(const fa_diff_lambda& l) {
+  return l.dtype == FA_LAMBDA_FP32 ? fa::kLamF32 : l.dtype == FA_BF16 ? fa::kLamBF16 : fa::kLamF16;
+}
+void lam_strides(int64_t (&s)[3], const fa_diff_lambda& l) {
+  s[0] = l.extent_b == 1 ? 0 : l.stride_b;
+  s[1] = l.extent_s == 1 ? 0 : l.stride_s;
+  s[2] = l.extent_h == 1 ? 0 : l.stride_h;
+}
+
+// Maps of q_1, q_2, k_1, k_2, v (and dO): 128 x 64-column boxes, query boxes of
+// `q_rows` rows.
+template <typename P>
+int diff_maps(const P* p, int q_rows, CUtensorMap (&m)[5]) {
+  int st;
+  for (int c = 0; c < 2; ++c) {
+    if ((st = make_map(&m[c], p->q[c], p->B, p->Sq, p->H, p->D, p->dtype, q_rows)) != FA_OK) return st;
+    if ((st = make_map(&m[2 + c], p->k[c], p->B, p->Sk, p->Hk, p->D, p->dtype, 128)) != FA_OK) return st;
+  }
+  return make_map(&m[4], p->v, p->B, p->Sk, p->Hk, p->Dv, p->dtype, 128);
+}
+
+template <int DV, bool BF16>
+int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
+  using L = fa::DiffFwdLayout<DV>;
+  static bool done[kMaxDevices] = {};
+  auto* kern = &fa::fa_diff_fwd_kernel<DV, BF16>;
+  int st = prepare(kern, L::SMEM_ALLOC, done);
+  if (st != FA_OK) return st;
+  CUtensorMap m[5];
+  if ((st = diff_maps(p, 128, m)) != FA_OK) return st;
+  fa::DiffFwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.o = p->o.ptr;
+  a.o2 = p->o2.ptr;
+  a.lse = p->lse;
+  set_strides(a.o_s, p->o);
+  set_strides(a.o2_s, p->o2);
+  a.lam = p->lambda.ptr;
+  lam_strides(a.lam_s, p->lambda);
+  a.lam_kind = lam_kind(p->lambda);
+  a.k_lens = p->k_lens;
+  a.B = p->B, a.H = p->H, a.Hk = p->Hk, a.Sq = p->Sq, a.Sk = p->Sk;
+  a.dv = p->Dv;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.causal = p->causal;
+  a.n_qblocks = (p->Sq + 127) / 128;
+  const unsigned grid = unsigned(int64_t(a.n_qblocks) * p->B * p->H);
+  kern<<<grid, L::kThreads, L::SMEM_ALLOC, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Workspace of the backward: dQ accumulators (or, deterministic, the slots),
+// the row terms, -Delta_2 per row, dlambda's partial sums; 256-byte aligned.
+struct DiffBwdWs {
+  uint64_t off_vec, off_drow, off_part, bytes;
+};
+constexpr int kLamParts = 1024;
+DiffBwdWs diff_bwd_ws(int B, int H, int Sq, int Sk, int deterministic) {
+  const uint64_t nq = (uint64_t(Sq) + 127) / 128, nk = (uint64_t(Sk) + 127) / 128;
+  const uint64_t rows = uint64_t(B) * H * nq * 128;
+  DiffBwdWs w;
+  w.off_vec = deterministic ? uint64_t(B) * H * nq * nk * 2 * 128 * 64 * 4 : rows * 2 * 64 * 4;
+  w.off_drow = w.off_vec + rows * 5 * 4;
+  w.off_part = round256(w.off_drow + uint64_t(B) * H * Sq * 4);
+  w.bytes = w.off_part + uint64_t(kLamParts) * 4;
+  return w;
+}
+
+int launch_lam(const fa_diff_bwd_params* p, const float* drow, float* part, cudaStream_t stream) {
+  fa::LamSumArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.drow = drow;
+  a.part = part;
+  a.dlam = p->dlambda;
+  a.dlam_kind = lam_kind(p->lambda);
+  a.B = p->B, a.H = p->H, a.Sq = p->Sq;
+  a.ext[0] = p->lambda.extent_b, a.ext[1] = p->lambda.extent_s, a.ext[2] = p->lambda.extent_h;
+  a.n_out = int64_t(a.ext[0]) * a.ext[1] * a.ext[2];
+  a.count = int64_t(a.B) * a.H * a.Sq / a.n_out;
+  if (a.count == 1) {
+    fa::fa_diff_lam_copy<<<unsigned((a.n_out + 255) / 256), 256, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  }
+  // Long sums of few elements are cut into runs of 2048 terms or more, at most
+  // kLamParts in all, and joined by a second kernel.
+  a.parts = int(std::max<int64_t>(1, std::min<int64_t>(kLamParts / a.n_out, a.count / 2048)));
+  fa::fa_diff_lam_part<<<unsigned(a.n_out * a.parts), 256, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (a.parts > 1) fa::fa_diff_lam_sum<<<unsigned(a.n_out), 256, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int DV, bool BF16>
+int launch_diff_bwd(const fa_diff_bwd_params* p, cudaStream_t stream) {
+  using L = fa::DiffBwdLayout<DV>;
+  static bool done[kMaxDevices] = {}, done_pre[kMaxDevices] = {}, done_dq[kMaxDevices] = {};
+  static bool done_det[kMaxDevices] = {};
+  auto* kern = &fa::fa_diff_bwd_main<DV, BF16>;
+  int st = prepare(kern, L::SMEM_ALLOC, done);
+  if (st != FA_OK) return st;
+  if ((st = prepare(&fa::fa_diff_pre<DV, BF16>, 0, done_pre)) != FA_OK) return st;
+  if ((st = prepare(&fa::fa_diff_dq<BF16, false>, 0, done_dq)) != FA_OK) return st;
+  if ((st = prepare(&fa::fa_diff_dq<BF16, true>, 0, done_det)) != FA_OK) return st;
+  CUtensorMap m[5], mdo;
+  if ((st = diff_maps(p, 64, m)) != FA_OK) return st;
+  if ((st = make_map(&mdo, p->dO, p->B, p->Sq, p->H, p->Dv, p->dtype, 64)) != FA_OK) return st;
+  fa::DiffBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.o = p->o.ptr, a.o2 = p->o2.ptr, a.dO = p->dO.ptr;
+  a.lse = p->lse;
+  a.lam = p->lambda.ptr;
+  lam_strides(a.lam_s, p->lambda);
+  a.lam_kind = lam_kind(p->lambda);
+  set_strides(a.o_s, p->o);
+  set_strides(a.o2_s, p->o2);
+  set_strides(a.do_s, p->dO);
+  for (int c = 0; c < 2; ++c) {
+    a.dq[c] = p->dq[c].ptr;
+    a.dk[c] = p->dk[c].ptr;
+    set_strides(a.dq_s[c], p->dq[c]);
+    set_strides(a.dk_s[c], p->dk[c]);
+  }
+  a.dv = p->dv.ptr;
+  set_strides(a.dv_s, p->dv);
+  a.B = p->B, a.H = p->H, a.Hk = p->Hk, a.Sq = p->Sq, a.Sk = p->Sk;
+  a.Sq_pad = (p->Sq + 127) / 128 * 128;
+  a.nqb = (p->Sq + 127) / 128;
+  a.nkb = (p->Sk + 127) / 128;
+  a.d = p->D;
+  a.dv_cols = p->Dv;
+  a.scale = p->scale;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.causal = p->causal;
+  const DiffBwdWs w = diff_bwd_ws(p->B, p->H, p->Sq, p->Sk, p->deterministic);
+  char* ws = static_cast<char*>(p->workspace);
+  a.dq_acc = reinterpret_cast<float*>(ws);
+  a.dq_part = p->deterministic ? reinterpret_cast<float*>(ws) : nullptr;
+  a.vec = reinterpret_cast<float*>(ws + w.off_vec);
+  a.drow = reinterpret_cast<float*>(ws + w.off_drow);
+  const int64_t rows = int64_t(p->B) * p->H * a.Sq_pad;
+  fa::fa_diff_pre<DV, BF16><<<unsigned(rows * (DV / 8) / 256), 256, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  CUtensorMap mdq = m[0];  // not read in deterministic mode
+  if (!p->deterministic && (st = make_dq_map(&mdq, a.dq_acc, 2 * rows, 64)) != FA_OK) return st;
+  const unsigned grid = unsigned(int64_t(a.nkb) * p->B * p->Hk);
+  kern<<<grid, L::kThreads, L::SMEM_ALLOC, stream>>>(m[0], m[1], m[2], m[3], m[4], mdo, mdq, a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  const dim3 dq_grid(unsigned((int64_t(p->B) * p->H * p->Sq * 8 + 255) / 256), 2);
+  if (p->deterministic)
+    fa::fa_diff_dq<BF16, true><<<dq_grid, 256, 0, stream>>>(a);
+  else
+    fa::fa_diff_dq<BF16, false><<<dq_grid, 256, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_lam(p, a.drow, reinterpret_cast<float*>(ws + w.off_part), stream);
+}
+
+template <bool BF16>
+int launch_rotary(const fa_rotary_params* p, cudaStream_t stream) {
+  fa::RotArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const fa_tensor* in[2] = {&p->q, &p->k};
+  const fa_tensor* out[2] = {&p->q_out, &p->k_out};
+  for (int i = 0; i < 2; ++i) {
+    a.x[i] = static_cast<const uint16_t*>(in[i]->ptr);
+    a.y[i] = static_cast<uint16_t*>(out[i]->ptr);
+    set_strides(a.xs[i], *in[i]);
+    set_strides(a.ys[i], *out[i]);
+  }
+  a.heads[0] = p->H;
+  a.heads[1] = p->Hk;
+  a.pos = p->positions;
+  a.pos_s[0] = p->pos_stride_axis, a.pos_s[1] = p->pos_stride_b, a.pos_s[2] = p->pos_stride_s;
+  a.pos64 = p->pos_int64;
+  a.inv_freq = p->inv_freq;
+  a.freq64 = p->inv_freq_fp64;
+  a.axes = p->axes;
+  for (int i = 0; i < p->axes; ++i) a.R += p->sections[i], a.end[i] = a.R;
+  a.B = p->B, a.S = p->S, a.D = p->D;
+  a.sign = p->inverse ? -1.f : 1.f;
+  // Tokens per block: about 16 KB of q and k, while the grid still covers the
+  // SMs; the sines and cosines stay within 16 KB.
+  const int64_t total = int64_t(p->B) * p->S;
+  const int64_t row_bytes = int64_t(p->H + p->Hk) * p->D * 2;
+  int64_t tokens = std::max<int64_t>(1, 16384 / row_bytes);
+  tokens = std::min<int64_t>(tokens, std::max<int64_t>(1, 2048 / a.R));
+  tokens = std::min<int64_t>(tokens, std::max<int64_t>(1, total / 592));
+  a.tokens = int(tokens);
+  const unsigned grid = unsigned((total + tokens - 1) / tokens);
+  const int smem = int(tokens) * a.R * int(sizeof(float2));
+  auto go = [&](auto* kern) {
+    kern<<<grid, 256, smem, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  };
+  if (p->interleaved) return go(&fa::fa_rotary_kernel<BF16, true, 8>);
+  if (a.R % 8 == 0) return go(&fa::fa_rotary_kernel<BF16, false, 8>);
+  if (a.R % 4 == 0) return go(&fa::fa_rotary_kernel<BF16, false, 4>);
+  if (a.R % 2 == 0) return go(&fa::fa_rotary_kernel<BF16, false, 2>);
+  return go(&fa::fa_rotary_kernel<BF16, false, 1>);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_diff_fwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, int causal) {
+  if (check_diff(B, H, Hk, Sq, Sk, D, Dv, 1.f, causal, FA_BF16) != FA_OK) return 0;
+  return 0;
+}
+
+int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream) {
+  if (p == nullptr) return FA_ERR_INVALID_ARG;
+  int st = check_diff(p->B, p->H, p->Hk, p->Sq, p->Sk, p->D, p->Dv, p->scale, p->causal, p->dtype);
+  if (st != FA_OK) return st;
+  for (int c = 0; c < 2; ++c) {
+    if ((st = check_view(p->q[c])) != FA_OK || (st = check_axes(p->q[c], p->B, p->Sq, p->H)) != FA_OK) return st;
+    if ((st = check_view(p->k[c])) != FA_OK || (st = check_axes(p->k[c], p->B, p->Sk, p->Hk)) != FA_OK) return st;
+  }
+  if ((st = check_view(p->v)) != FA_OK || (st = check_axes(p->v, p->B, p->Sk, p->Hk)) != FA_OK) return st;
+  if ((st = check_view(p->o)) != FA_OK || (st = check_axes(p->o, p->B, p->Sq, p->H)) != FA_OK) return st;
+  if ((st = check_view(p->o2, true)) != FA_OK) return st;
+  if (p->o2.ptr != nullptr && (st = check_axes(p->o2, p->B, p->Sq, p->H)) != FA_OK) return st;
+  if ((st = check_lam(p->lambda, p->B, p->Sq, p->H, p->dtype)) != FA_OK) return st;
+  if (p->lse == nullptr) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p->lse) & 3u) return FA_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(p->k_lens) & 3u) return FA_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->Dv <= 64) return p->dtype == FA_BF16 ? launch_diff_fwd<64, true>(p, s) : launch_diff_fwd<64, false>(p, s);
+  return p->dtype == FA_BF16 ? launch_diff_fwd<128, true>(p, s) : launch_diff_fwd<128, false>(p, s);
+}
+
+size_t fa_diff_bwd_workspace_size(int B, int H, int Sq, int Sk, int deterministic) {
+  if (deterministic != 0 && deterministic != 1) return 0;
+  if (check_diff(B, H, H, Sq, Sk, 64, 64, 1.f, 0, FA_BF16) != FA_OK) return 0;
+  const uint64_t bytes = diff_bwd_ws(B, H, Sq, Sk, deterministic).bytes;
+  return bytes > (uint64_t(1) << 50) ? 0 : size_t(bytes);
+}
+
+int fa_diff_bwd(const fa_diff_bwd_params* p, fa_stream_t stream) {
+  if (p == nullptr) return FA_ERR_INVALID_ARG;
+  int st = check_diff(p->B, p->H, p->Hk, p->Sq, p->Sk, p->D, p->Dv, p->scale, p->causal, p->dtype);
+  if (st != FA_OK) return st;
+  const fa_tensor* qs[8] = {&p->q[0], &p->q[1], &p->o, &p->o2, &p->dO, &p->dq[0], &p->dq[1], nullptr};
+  for (int i = 0; qs[i] != nullptr; ++i)
+    if ((st = check_view(*qs[i])) != FA_OK || (st = check_axes(*qs[i], p->B, p->Sq, p->H)) != FA_OK) return st;
+  const fa_tensor* ks[7] = {&p->k[0], &p->k[1], &p->v, &p->dk[0], &p->dk[1], &p->dv, nullptr};
+  for (int i = 0; ks[i] != nullptr; ++i)
+    if ((st = check_view(*ks[i])) != FA_OK || (st = check_axes(*ks[i], p->B, p->Sk, p->Hk)) != FA_OK) return st;
+  if ((st = check_lam(p->lambda, p->B, p->Sq, p->H, p->dtype)) != FA_OK) return st;
+  if (p->dlambda == nullptr || p->lse == nullptr) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p->dlambda) & (p->lambda.dtype == FA_LAMBDA_FP32 ? 3u : 1u)) return FA_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(p->lse) & 3u) return FA_ERR_MISALIGNED;
+  if (p->deterministic != 0 && p->deterministic != 1) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_diff_bwd_workspace_size(p->B, p->H, p->Sq, p->Sk, p->deterministic);
+  if (p->workspace == nullptr || p->workspace_bytes < need || need == 0) return FA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(p->workspace) & 255u) return FA_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->Dv <= 64) return p->dtype == FA_BF16 ? launch_diff_bwd<64, true>(p, s) : launch_diff_bwd<64, false>(p, s);
+  return p->dtype == FA_BF16 ? launch_diff_bwd<128, true>(p, s) : launch_diff_bwd<128, false>(p, s);
+}
+
+int fa_rotary(const fa_rotary_params* p, fa_stream_t stream) {
+  if (p == nullptr) return FA_ERR_INVALID_ARG;
+  if (p->B < 1 || p->S < 1 || p->H < 1 || p->Hk < 0) return FA_ERR_INVALID_ARG;
+  if (p->dtype != FA_FP16 && p->dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+  if (p->D < 8 || p->D > 256 || p->D % 8) return FA_ERR_UNSUPPORTED;
+  const int64_t lim = (int64_t(1) << 31) - 1;
+  if (int64_t(p->B) * p->S > lim || int64_t(p->H) + p->Hk > 65536) return FA_ERR_INVALID_ARG;
+  if (p->axes < 1 || p->axes > FA_ROTARY_MAX_AXES) return FA_ERR_INVALID_ARG;
+  int64_t pairs = 0;
+  for (int i = 0; i < p->axes; ++i) {
+    if (p->sections[i] < 0) return FA_ERR_INVALID_ARG;
+    pairs += p->sections[i];
+  }
+  if (pairs < 1 || 2 * pairs > p->D) return FA_ERR_INVALID_ARG;
+  if ((p->interleaved | 1) != 1 || (p->inverse | 1) != 1 || (p->pos_int64 | 1) != 1 || (p->inv_freq_fp64 | 1) != 1)
+    return FA_ERR_INVALID_ARG;
+  const fa_tensor* t[4] = {&p->q, &p->q_out, &p->k, &p->k_out};
+  for (int i = 0; i < (p->Hk > 0 ? 4 : 2); ++i) {
+    int st = check_view(*t[i]);
+    if (st != FA_OK) return st;
+    if ((i & 1) && (st = check_axes(*t[i], p->B, p->S, i < 2 ? p->H : p->Hk)) != FA_OK) return st;
+  }
+  if (p->positions == nullptr || p->inv_freq == nullptr) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p->positions) & (p->pos_int64 ? 7u : 3u)) return FA_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(p->inv_freq) & (p->inv_freq_fp64 ? 7u : 3u)) return FA_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return p->dtype == FA_BF16 ? launch_rotary<true>(p, s) : launch_rotary<false>(p, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,806 @@
+// fa_diff_bwd.cuh — differential attention backward for sm_100a (fa_diff_bwd).
+//
+// With P_c = softmax(scale Q_c K_c^T), O_c = P_c V, O = O_1 - lambda O_2 and
+// W = P_1 - lambda P_2:
+//   dV = W^T dO,   dP = dO V^T (one product serves both maps),
+//   Delta_c = rowsum(P_c dP) = dO . O_c   (O_1 = O + lambda O_2),
+//   dS_1 = P_1 (dP - Delta_1),   dS_2 = -lambda P_2 (dP - Delta_2),
+//   dQ_c = scale dS_c K_c,   dK_c = scale dS_c^T Q_c,
+//   dlambda = -dO . O_2 = -Delta_2.
+// Two plain attention backwards would run dP and dV twice; taken together a
+// 128 x 128 block costs 2 x 128 x 128 x (6 x 64 + 2 DV) flops, 640 columns of
+// products at DV = 128 instead of 896.
+//
+// Kernels on the caller's stream:
+//  1. fa_diff_pre: per row Delta_1, Delta_2, both LSEs in base 2 (+inf for rows
+//     with no key and padding rows) and -lambda, packed per 64 rows; zeroes
+//     the fp32 dQ accumulators; writes -Delta_2 per row for dlambda.
+//  2. fa_diff_bwd_main: one CTA per (batch, key head, 128-key block); walks the
+//     query blocks of every query head that shares the key head, so dK and dV
+//     of shared heads are summed in the CTA's fp32 accumulators, in a fixed
+//     order.
+//  3. fa_diff_dq: dq_c = scale * accumulator, rounded to the input dtype.
+//  4. fa_diff_lam_part / fa_diff_lam_sum: dlambda, summed over the axes lambda
+//     is broadcast over in a fixed order.
+//
+// Main kernel. Query rows go through the softmax 64 at a time ("chunks", two
+// per 128-row query block): S_1^T, S_2^T and dP^T of a chunk then take 3 x 64
+// columns of tensor memory beside the accumulators dV, dK_1, dK_2 (256) and a
+// dQ block of one map (64 columns), 512 in all, and the shared memory holds
+// two stages of Q_1, Q_2 and dO. dQ is a product over whole 128-row blocks (M
+// = 128 is the tensor core's full rate), taken after the second chunk from the
+// two dS^T halves in shared memory.
+//
+// Warp roles (448 threads):
+//   warps 0-7   one key row per thread; warps 0-3 take query columns [0, 32)
+//               of the chunk, warps 4-7 [32, 64). P_1 and -lambda P_2 stay in
+//               fp32 registers between the two phases of a chunk. At the end
+//               warps 0-3 write dK_1 and dK_2, warps 4-7 dV.
+//   warps 8-11  read the dQ blocks out of tensor memory (one query row per
+//               thread) and add them into the fp32 accumulators through the
+//               TMA; deterministic mode stores them into their own slots.
+//   warp  12    TMA loader: K_1, K_2, V once; Q_1, Q_2 with the row terms, and
+//               dO, per chunk
+//   warp  13    MMA issuer
+// MMA order per chunk i: dV(i), S_1(i+1), S_2(i+1), [dQ_1], dK_1(i), dK_2(i),
+// dP(i+1), [dQ_2], with dQ after odd chunks: the softmax of chunk i+1 starts
+// while dK(i), dP(i+1) and dQ run.
+#pragma once
+
+#include <type_traits>
+
+#include "fa_common.cuh"
+#include "fa_diff_fwd.cuh"
+
+namespace fa {
+
+struct DiffBwdArgs {
+  const void* o;
+  const void* o2;
+  const void* dO;
+  const float* lse;  // [2][B][H][Sq]
+  const void* lam;
+  int64_t lam_s[3];
+  int lam_kind;
+  void* dq[2];
+  void* dk[2];
+  void* dv;
+  int64_t o_s[3], o2_s[3], do_s[3], dq_s[2][3], dk_s[2][3], dv_s[3];
+  float* dq_acc;   // fp32 [2][B*H][Sq_pad][64]
+  float* vec;      // fp32 [B*H][Sq_pad / 64][5][64]: lse2_1, lse2_2, -lambda, Delta_1, Delta_2
+  float* drow;     // fp32 [B][H][Sq]: -Delta_2
+  float* dq_part;  // deterministic mode: fp32 [B*H][nqb][nkb][2][128][64] slots; else null
+  int B, H, Hk, Sq, Sk, Sq_pad;
+  int nqb, nkb;    // ceil(Sq / 128), ceil(Sk / 128)
+  int d, dv_cols;  // head_dim of q and k; columns of v
+  float scale, scale_log2;
+  int causal;
+};
+
+constexpr int kDiffVec = 5 * 64;  // floats of one chunk's row terms
+
+// ------------------------------------------------------------- preprocess
+// DV / 8 threads per (b, h, i) row, i in [0, Sq_pad).
+template <int DV, bool BF16>
+__global__ void __launch_bounds__(256) fa_diff_pre(const DiffBwdArgs a) {
+  constexpr int G = DV / 8;
+  const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t row = gid / G;
+  const int part = static_cast<int>(gid % G);
+  const int64_t nrows = static_cast<int64_t>(a.B) * a.H * a.Sq_pad;
+  if (row >= nrows) return;  // whole groups leave together: G divides 32, nrows * G is a multiple of 256
+  const int i = static_cast<int>(row % a.Sq_pad);
+  const int bh = static_cast<int>(row / a.Sq_pad);
+  const int h = bh % a.H;
+  const int b = bh / a.H;
+  float d_o = 0.f, d_2 = 0.f;  // dO . O, dO . O_2
+  if (i < a.Sq && part * 8 < a.dv_cols && checked(b < a.B && h < a.H, 501)) {
+    auto at = [&](const void* p, const int64_t(&s)[3]) {
+      return *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + b * s[0] + i * s[1] + h * s[2] +
+                                             part * 8);
+    };
+    const uint4 ov = at(a.o, a.o_s), o2v = at(a.o2, a.o2_s), gv = at(a.dO, a.do_s);
+    const uint32_t* o32 = reinterpret_cast<const uint32_t*>(&ov);
+    const uint32_t* p32 = reinterpret_cast<const uint32_t*>(&o2v);
+    const uint32_t* g32 = reinterpret_cast<const uint32_t*>(&gv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = sm100::unpack2<BF16>(o32[k]);
+      const float2 z = sm100::unpack2<BF16>(p32[k]);
+      const float2 y = sm100::unpack2<BF16>(g32[k]);
+      d_o = fmaf(x.x, y.x, d_o);
+      d_o = fmaf(x.y, y.y, d_o);
+      d_2 = fmaf(z.x, y.x, d_2);
+      d_2 = fmaf(z.y, y.y, d_2);
+    }
+  }
+#pragma unroll
+  for (int s = G / 2; s > 0; s >>= 1) {
+    d_o += __shfl_xor_sync(0xffffffffu, d_o, s);
+    d_2 += __shfl_xor_sync(0xffffffffu, d_2, s);
+  }
+  if (a.dq_part == nullptr && checked(row < nrows, 502)) {  // the atomic accumulators start from zero
+    constexpr int F4 = 64 * 2 / 4 / G;  // float4s per thread over both maps
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < F4; ++u) {
+      const int f = part + u * G;  // 0 .. 31: map f / 16, float4 f % 16
+      reinterpret_cast<float4*>(a.dq_acc)[((f >> 4) * nrows + row) * 16 + (f & 15)] = z;
+    }
+  }
+  if (part == 0 && checked(row < nrows, 503)) {
+    float l1 = INFINITY, l2 = INFINITY, lam = 0.f;
+    if (i < a.Sq) {
+      const int64_t at = static_cast<int64_t>(bh) * a.Sq + i;
+      const float e1 = a.lse[at], e2 = a.lse[static_cast<int64_t>(a.B) * a.H * a.Sq + at];
+      if (e1 != -INFINITY) {  // a row with no key has -inf in both
+        l1 = e1 * 1.4426950408889634f;
+        l2 = e2 * 1.4426950408889634f;
+        lam = load_lam(a.lam, a.lam_kind, b * a.lam_s[0] + i * a.lam_s[1] + h * a.lam_s[2]);
+      } else {
+        d_o = d_2 = 0.f;
+      }
+      a.drow[at] = -d_2;
+    }
+    float* v = a.vec + (static_cast<int64_t>(bh) * (a.Sq_pad / 64) + i / 64) * kDiffVec + (i & 63);
+    v[0] = l1;
+    v[64] = l2;
+    v[128] = -lam;
+    v[192] = lam == 0.f ? d_o : fmaf(lam, d_2, d_o);
+    v[256] = d_2;
+  }
+}
+
+// ------------------------------------------------------------- dq convert
+// dq_c = scale * accumulator (or the key blocks' slots, added in key-block
+// order). 8 columns per thread; map in blockIdx.y.
+template <bool BF16, bool DET>
+__global__ void __launch_bounds__(256) fa_diff_dq(const DiffBwdArgs a) {
+  const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t row = gid / 8;  // (b, h, i) with i < Sq
+  const int part = static_cast<int>(gid % 8);
+  const int c = blockIdx.y;
+  const int64_t bhs = static_cast<int64_t>(a.B) * a.H;
+  if (row >= bhs * a.Sq || part * 8 >= a.d) return;
+  const int i = static_cast<int>(row % a.Sq);
+  const int bh = static_cast<int>(row / a.Sq);
+  const int h = bh % a.H;
+  const int b = bh / a.H;
+  float acc[8];
+  if constexpr (DET) {
+    const int qb = i / 128;
+    const float* slot =
+        a.dq_part + ((static_cast<int64_t>(bh) * a.nqb + qb) * a.nkb * 2 + c) * (128 * 64) + (i % 128) * 64 + part * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int kvb = 0; kvb < a.nkb; ++kvb) {
+      if (qb < bwd_first_qblock(kvb, a.Sq, a.Sk, a.causal)) break;  // later key blocks start later still
+      const float4* src = reinterpret_cast<const float4*>(slot + static_cast<int64_t>(kvb) * (2 * 128 * 64));
+      const float4 x = src[0], y = src[1];
+      acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+      acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+    }
+  } else {
+    const float4* src = reinterpret_cast<const float4*>(a.dq_acc + ((c * bhs + bh) * a.Sq_pad + i) * 64 + part * 8);
+    const float4 x = src[0], y = src[1];
+    acc[0] = x.x, acc[1] = x.y, acc[2] = x.z, acc[3] = x.w;
+    acc[4] = y.x, acc[5] = y.y, acc[6] = y.z, acc[7] = y.w;
+  }
+  const float s = a.scale;
+  uint4 out;
+  out.x = sm100::pack2<BF16>(acc[0] * s, acc[1] * s);
+  out.y = sm100::pack2<BF16>(acc[2] * s, acc[3] * s);
+  out.z = sm100::pack2<BF16>(acc[4] * s, acc[5] * s);
+  out.w = sm100::pack2<BF16>(acc[6] * s, acc[7] * s);
+  if (checked(b < a.B && h < a.H && i < a.Sq, 504))
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.dq[c]) + b * a.dq_s[c][0] + i * a.dq_s[c][1] +
+                              h * a.dq_s[c][2] + part * 8) = out;
+}
+
+// ----------------------------------------------------------- dlambda sums
+// dlambda has extents ext[] (each 1 or the full axis; order batch, row, head)
+// and is dense. Element x sums drow over the axes with extent 1: `count` terms,
+// cut into `parts` runs. One block per (element, run) writes its sum to
+// part[element * parts + run], in a fixed order.
+struct LamSumArgs {
+  const float* drow;  // [B][H][Sq]
+  float* part;
+  void* dlam;
+  int dlam_kind;
+  int B, H, Sq;
+  int ext[3];
+  int64_t n_out, count;
+  int parts;
+};
+
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, float* sm) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float r = 0.f;
+  for (int w = 0; w < THREADS / 32; ++w) r += sm[w];
+  __syncthreads();
+  return r;
+}
+
+__device__ __forceinline__ void store_lam(void* p, int kind, int64_t at, float v) {
+  if (kind == kLamF32)
+    static_cast<float*>(p)[at] = v;
+  else
+    static_cast<uint16_t*>(p)[at] =
+        static_cast<uint16_t>((kind == kLamBF16 ? sm100::pack2<true>(v, 0.f) : sm100::pack2<false>(v, 0.f)) & 0xffffu);
+}
+
+// No axis is broadcast: one thread per element.
+__global__ void __launch_bounds__(256) fa_diff_lam_copy(const LamSumArgs a) {
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // [B][Sq][H]
+  if (x >= a.n_out) return;
+  const int h = static_cast<int>(x % a.H);
+  const int64_t bs = x / a.H;
+  const int64_t b = bs / a.Sq, s = bs - b * a.Sq;
+  store_lam(a.dlam, a.dlam_kind, x, a.drow[(b * a.H + h) * a.Sq + s]);
+}
+
+__global__ void __launch_bounds__(256) fa_diff_lam_part(const LamSumArgs a) {
+  __shared__ float sm[8];
+  const int64_t x = blockIdx.x / a.parts;
+  const int run = static_cast<int>(blockIdx.x % a.parts);
+  const int eh = static_cast<int>(x % a.ext[2]);
+  const int64_t y = x / a.ext[2];
+  const int es = static_cast<int>(y % a.ext[1]), eb = static_cast<int>(y / a.ext[1]);
+  // The summed axes, innermost first: rows, heads, batch.
+  const int ns = a.ext[1] == 1 ? a.Sq : 1, nh = a.ext[2] == 1 ? a.H : 1;
+  const int64_t len = (a.count + a.parts - 1) / a.parts;
+  const int64_t lo = run * len, hi = min(a.count, lo + len);
+  float v = 0.f;
+  for (int64_t k = lo + threadIdx.x; k < hi; k += 256) {
+    const int64_t s = k % ns, z = k / ns;
+    const int64_t h = z % nh, b = z / nh;
+    v += a.drow[((eb + b) * a.H + eh + h) * a.Sq + es + s];
+  }
+  v = block_sum<256>(v, sm);
+  if (threadIdx.x == 0) {
+    if (a.parts == 1)
+      store_lam(a.dlam, a.dlam_kind, x, v);
+    else
+      a.part[blockIdx.x] = v;
+  }
+}
+
+__global__ void __launch_bounds__(256) fa_diff_lam_sum(const LamSumArgs a) {
+  __shared__ float sm[8];
+  float v = 0.f;
+  for (int k = threadIdx.x; k < a.parts; k += 256) v += a.part[static_cast<int64_t>(blockIdx.x) * a.parts + k];
+  v = block_sum<256>(v, sm);
+  if (threadIdx.x == 0) store_lam(a.dlam, a.dlam_kind, blockIdx.x, v);
+}
+
+// ------------------------------------------------------------- main kernel
+template <int DV>
+struct DiffBwdLayout {
+  static constexpr int kThreads = 448;
+  static constexpr int BLK = 128 * 128;   // [128 rows][64 columns] of 16 bits
+  static constexpr int HBLK = 64 * 128;   // [64 rows][64 columns]
+  static constexpr int VB = DV / 64;
+  static constexpr int ST = 2;            // stages of (Q_1, Q_2, row terms) and of dO
+  static constexpr int OFF_K = 0;                       // K_1, K_2
+  static constexpr int OFF_V = OFF_K + 2 * BLK;
+  static constexpr int OFF_Q = OFF_V + VB * BLK;        // [stage][map][64 rows]
+  static constexpr int OFF_DO = OFF_Q + ST * 2 * HBLK;  // [stage][column block][64 rows]
+  static constexpr int OFF_DS = OFF_DO + ST * VB * HBLK;  // dS_c^T: [map][chunk half][128 keys][64 queries]
+  static constexpr int OFF_DQS = OFF_DS + 4 * BLK;      // dQ staging: 4 KB per drain warp
+  static constexpr int OFF_VEC = OFF_DQS + 4 * 4096;
+  static constexpr int OFF_BAR = OFF_VEC + ST * kDiffVec * 4;
+  // kv_full, q_full/q_empty[ST], o_full/o_empty[ST], s_full, w_ready, dp_full, ds_ready, ds_free, dq_full,
+  // dq_free, mma_done, drain
+  static constexpr int NBAR = 1 + 4 * ST + 9;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int SMEM_ALLOC = BYTES + 1024;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int COL_DV = 0;
+  static constexpr int COL_DK = 128;  // dK_1, dK_2: 64 columns each
+  static constexpr int COL_S = 256;   // S_1^T, S_2^T: 64 columns each; W^T over S_1^T
+  static constexpr int COL_DP = 384;
+  static constexpr int COL_DQ = 448;
+};
+
+template <int DV, bool BF16>
+__global__ void __launch_bounds__(448, 1)
+    fa_diff_bwd_main(const __grid_constant__ CUtensorMap tmQ1, const __grid_constant__ CUtensorMap tmQ2,
+                     const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmK2,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                     const __grid_constant__ CUtensorMap tmDQ, const DiffBwdArgs a) {
+  using L = DiffBwdLayout<DV>;
+  using namespace sm100;
+  constexpr int ST = L::ST;
+  static_assert(L::SMEM_ALLOC <= 232448, "smem budget");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* q_full = kv_full + 1;
+  uint64_t* q_empty = q_full + ST;
+  uint64_t* o_full = q_empty + ST;
+  uint64_t* o_empty = o_full + ST;
+  uint64_t* s_full = o_empty + ST;
+  uint64_t* w_ready = s_full + 1;
+  uint64_t* dp_full = w_ready + 1;
+  uint64_t* ds_ready = dp_full + 1;
+  uint64_t* ds_free = ds_ready + 1;
+  uint64_t* dq_full = ds_free + 1;
+  uint64_t* dq_free = dq_full + 1;
+  uint64_t* mma_done = dq_free + 1;
+  uint64_t* drain = mma_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  const float* s_vec = reinterpret_cast<const float*>(smem + L::OFF_VEC);
+  constexpr int kLoaderWarp = 12, kMmaWarp = 13;
+
+  // Grid order as the plain backward's: with a causal mask key-block-major,
+  // the first key blocks (the most query blocks) first; without one
+  // head-major.
+  const int hb_count = a.Hk * a.B;
+  const int kvb = a.causal ? static_cast<int>(blockIdx.x) / hb_count : static_cast<int>(blockIdx.x) % a.nkb;
+  const int hb = a.causal ? static_cast<int>(blockIdx.x) % hb_count : static_cast<int>(blockIdx.x) / a.nkb;
+  const int hk = hb % a.Hk;
+  const int b = hb / a.Hk;
+  const int group = a.H / a.Hk;
+  const int n0 = kvb * 128;
+  const int off = a.Sk - a.Sq;
+  const int i_start = bwd_first_qblock(kvb, a.Sq, a.Sk, a.causal);
+  const int nb = max(0, a.nqb - i_start);  // query blocks of one head
+  const int n = 2 * nb * group;            // chunks
+  // Chunk i: its head's (b, h) row base and its first query row.
+  auto chunk_bh = [&](int i) { return b * a.H + hk * group + (i >> 1) / nb; };
+  auto chunk_row = [&](int i) { return (i_start + (i >> 1) % nb) * 128 + (i & 1) * 64; };
+  const int64_t acc_rows = static_cast<int64_t>(a.B) * a.H * a.Sq_pad;  // of one map's dQ accumulator
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&o_full[s], 1);
+      mbar_init(&o_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(w_ready, 256);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 256);
+    mbar_init(ds_free, 1);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_free, 128);
+    mbar_init(mma_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kLoaderWarp && lane == 0) {
+    prefetch_tmap(&tmQ1);
+    prefetch_tmap(&tmQ2);
+    prefetch_tmap(&tmK1);
+    prefetch_tmap(&tmK2);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmdO);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kLoaderWarp) {
+    // ------------------------------------------------------------------ loader
+    if (lane == 0 && n > 0) {
+      checked(n0 < a.Sk && b < a.B && hk < a.Hk, 510);
+      mbar_arrive_expect_tx(kv_full, (2 + L::VB) * L::BLK);
+      tma_load_4d(smem + L::OFF_K, &tmK1, kv_full, 0, n0, hk, b);
+      tma_load_4d(smem + L::OFF_K + L::BLK, &tmK2, kv_full, 0, n0, hk, b);
+      for (int vb = 0; vb < L::VB; ++vb)
+        tma_load_4d(smem + L::OFF_V + vb * L::BLK, &tmV, kv_full, vb * 64, n0, hk, b);
+      int nq = 0, no = 0;  // loads issued
+      auto load_q = [&](int i) -> bool {
+        const int st = i % ST;
+        if (!wait_bar(&q_empty[st], ((i / ST) & 1) ^ 1, abort_flag, kRoleLoader, i)) return false;
+        const int bh = chunk_bh(i), r0 = chunk_row(i), h = bh - b * a.H;
+        mbar_arrive_expect_tx(&q_full[st], 2 * L::HBLK + kDiffVec * 4);
+        tma_load_4d(smem + L::OFF_Q + st * 2 * L::HBLK, &tmQ1, &q_full[st], 0, r0, h, b);
+        tma_load_4d(smem + L::OFF_Q + (st * 2 + 1) * L::HBLK, &tmQ2, &q_full[st], 0, r0, h, b);
+        // Skipped on a failed check: its wait then runs out (FA_ERR_BOUNDS stays recorded).
+        if (checked(r0 + 64 <= a.Sq_pad && h < a.H, 511))
+          bulk_load(smem + L::OFF_VEC + st * kDiffVec * 4,
+                    a.vec + (static_cast<int64_t>(bh) * (a.Sq_pad / 64) + r0 / 64) * kDiffVec, kDiffVec * 4,
+                    &q_full[st]);
+        ++nq;
+        return true;
+      };
+      auto load_o = [&](int i) -> bool {
+        const int st = i % ST;
+        if (!wait_bar(&o_empty[st], ((i / ST) & 1) ^ 1, abort_flag, kRoleLoader, i)) return false;
+        const int h = chunk_bh(i) - b * a.H, r0 = chunk_row(i);
+        mbar_arrive_expect_tx(&o_full[st], L::VB * L::HBLK);
+        for (int vb = 0; vb < L::VB; ++vb)
+          tma_load_4d(smem + L::OFF_DO + (st * L::VB + vb) * L::HBLK, &tmdO, &o_full[st], vb * 64, r0, h, b);
+        ++no;
+        return true;
+      };
+      bool lok = true;
+      for (int i = 0; lok && i < n; ++i) {
+        lok = load_o(i);  // a stage of dO frees before the same chunk's stage of Q
+        if (lok) lok = load_q(i);
+      }
+      if (*abort_flag) {
+        drain_wait(kv_full, 0);
+        for (int i = max(0, nq - ST); i < nq; ++i) drain_wait(&q_full[i % ST], (i / ST) & 1);
+        for (int i = max(0, no - ST); i < no; ++i) drain_wait(&o_full[i % ST], (i / ST) & 1);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- MMA issuer
+    if (n > 0) {
+      auto wait = [&](uint64_t* bar, uint32_t parity, int iter) {
+        return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, kRoleMma, iter));
+      };
+      const uint32_t sK = smem_u32(smem + L::OFF_K);
+      const uint32_t sV = smem_u32(smem + L::OFF_V);
+      const uint32_t sQ = smem_u32(smem + L::OFF_Q);
+      const uint32_t sdO = smem_u32(smem + L::OFF_DO);
+      const uint32_t sDS = smem_u32(smem + L::OFF_DS);
+      // S_c^T = K_c Q_c^T, dP^T = V dO^T: M = 128 keys, N = 64 queries (both K-major).
+      constexpr uint32_t id_s = idesc_f16(BF16, 128, 64, 0, 0);
+      // dV += W^T dO (A in TMEM), dK_c += dS_c^T Q_c (A in smem, K-major); B MN-major, K = 64 queries.
+      constexpr uint32_t id_v = idesc_f16(BF16, 128, DV, 0, 1);
+      constexpr uint32_t id_k = idesc_f16(BF16, 128, 64, 0, 1);
+      // dQ_c = dS_c K_c: M = 128 queries, N = 64, K = 128 keys; A = dS_c^T viewed MN-major, B = K_c MN-major.
+      constexpr uint32_t id_q = idesc_f16(BF16, 128, 64, 1, 1);
+      auto issue_S = [&](int st) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t a0 = desc_sw128(sK + c * L::BLK, 16, 1024);
+          const uint64_t b0 = desc_sw128(sQ + (st * 2 + c) * L::HBLK, 16, 1024);
+          uint64_t ad[4], bd[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ad[u] = desc_add(a0, u * 32), bd[u] = desc_add(b0, u * 32);
+          mma_ss_x4(tmem + L::COL_S + 64 * c, ad, bd, id_s, 0);
+        }
+      };
+      auto issue_dP = [&](int st) {
+#pragma unroll
+        for (int vb = 0; vb < L::VB; ++vb) {
+          const uint64_t a0 = desc_sw128(sV + vb * L::BLK, 16, 1024);
+          const uint64_t b0 = desc_sw128(sdO + (st * L::VB + vb) * L::HBLK, 16, 1024);
+          uint64_t ad[4], bd[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ad[u] = desc_add(a0, u * 32), bd[u] = desc_add(b0, u * 32);
+          mma_ss_x4(tmem + L::COL_DP, ad, bd, id_s, vb > 0);
+        }
+      };
+      auto issue_dV = [&](int st, uint32_t acc) {
+        const uint64_t b0 = desc_sw128(sdO + st * L::VB * L::HBLK, L::HBLK, 1024);
+        uint32_t pa[4];
+        uint64_t bd[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          pa[u] = tmem + L::COL_S + (u >> 1) * 32 + (u & 1) * 8;  // W^T of queries 16u .. 16u + 15
+          bd[u] = desc_add(b0, u * 2048);
+        }
+        mma_ts_x4(tmem + L::COL_DV, pa, bd, id_v, acc);
+      };
+      auto issue_dK = [&](int st, int hf, uint32_t acc) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t a0 = desc_sw128(sDS + (c * 2 + hf) * L::BLK, 16, 1024);
+          const uint64_t b0 = desc_sw128(sQ + (st * 2 + c) * L::HBLK, L::HBLK, 1024);
+          uint64_t ad[4], bd[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) ad[u] = desc_add(a0, u * 32), bd[u] = desc_add(b0, u * 2048);
+          mma_ss_x4(tmem + L::COL_DK + 64 * c, ad, bd, id_k, acc);
+        }
+      };
+      auto issue_dQ = [&](int c) {
+        const uint64_t a0 = desc_sw128(sDS + c * 2 * L::BLK, L::BLK, 1024);
+        const uint64_t b0 = desc_sw128(sK + c * L::BLK, L::BLK, 1024);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint64_t ad[4], bd[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            ad[u] = desc_add(a0, (4 * hf + u) * 2048);
+            bd[u] = desc_add(b0, (4 * hf + u) * 2048);
+          }
+          mma_ss_x4(tmem + L::COL_DQ, ad, bd, id_q, hf > 0);
+        }
+      };
+      bool ok = wait(kv_full, 0, -1) && wait(&q_full[0], 0, 0);
+      if (ok) {
+        tc_fence_after();
+        issue_S(0);
+        mma_commit_w(s_full);
+        ok = wait(&o_full[0], 0, 0);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_dP(0);
+        mma_commit_w(dp_full);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int st = i % ST, sn = (i + 1) % ST;
+        const uint32_t phn = ((i + 1) / ST) & 1;
+        const bool odd = i & 1;
+        const int blk = i >> 1;
+        if (!(ok = wait(w_ready, i & 1, i))) break;
+        tc_fence_after();
+        issue_dV(st, i > 0);
+        if (i + 1 < n) {
+          // S(i+1) goes over S(i) and W(i): the softmax warps have read S(i)
+          // (w_ready) and dV(i), issued before, reads W(i) first.
+          if (!(ok = wait(&q_full[sn], phn, i + 1))) break;
+          tc_fence_after();
+          issue_S(sn);
+          mma_commit_w(s_full);
+        }
+        if (!(ok = wait(ds_ready, i & 1, i))) break;
+        tc_fence_after();
+        mma_commit_w(&o_empty[st]);  // dV(i) and dP(i), issued before, were dO(i)'s last readers
+        if (odd) {
+          // The dQ buffer's use 2 blk + c waits for the drain of the use before.
+          if (blk > 0 && !(ok = wait(dq_free, (2 * blk - 1) & 1, i))) break;
+          tc_fence_after();
+          issue_dQ(0);
+          mma_commit_w(dq_full);
+        }
+        issue_dK(st, i & 1, i > 0);
+        mma_commit_w(&q_empty[st]);
+        if (i + 1 < n) {
+          if (!(ok = wait(&o_full[sn], phn, i + 1))) break;
+          tc_fence_after();
+          issue_dP(sn);
+          mma_commit_w(dp_full);
+        }
+        if (odd) {
+          if (!(ok = wait(dq_free, (2 * blk) & 1, i))) break;
+          tc_fence_after();
+          issue_dQ(1);
+          mma_commit_w(dq_full);
+          mma_commit_w(ds_free);
+        }
+      }
+      mma_commit_w(mma_done);
+      mma_commit_w(drain);
+      drain_wait(drain, 0);
+    }
+  } else if (warp < 8) {
+    // ------------------- P and dS: one key row per thread, 32 query columns per warpgroup
+    const int g = warp >> 2;
+    const int kr = (warp & 3) * 32 + lane;
+    const int key = n0 + kr;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS1 = tmem + lane_base + L::COL_S + 32 * g;
+    const uint32_t tDP = tmem + lane_base + L::COL_DP + 32 * g;
+    const float sl2 = a.scale_log2;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int st = i % ST;
+      ok = __all_sync(0xffffffffu, wait_bar(s_full, i & 1, abort_flag, kRoleSoftmax, i) &&
+                                       wait_bar(&q_full[st], (i / ST) & 1, abort_flag, kRoleSoftmax, i));
+      if (!ok) break;
+      tc_fence_after();
+      // Query columns e < cm of this warpgroup's 32 are masked for this key
+      // (causal); all of them if key >= Sk.
+      int cm = a.causal ? key - off - chunk_row(i) - 32 * g : -1;
+      if (key >= a.Sk) cm = 32;
+      const float* vec = s_vec + st * kDiffVec + 32 * g;
+      // Phase A: p1 = P_1^T, p2 = -lambda P_2^T (fp32, kept), W^T = p1 + p2 in
+      // 16 bits over S_1^T.
+      uint32_t p1[32], p2[32];
+      tmem_ld32(tS1, p1);
+      tmem_ld32(tS1 + 64, p2);
+      tmem_ld_wait();
+      reg_fence(p1);
+      reg_fence(p2);
+      {
+        uint32_t w[16];
+        auto block = [&](auto masked) {
+          const uint64_t sl2x2 = f2(sl2, sl2);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float4 la = reinterpret_cast<const float4*>(vec)[u];
+            const float4 lb = reinterpret_cast<const float4*>(vec + 64)[u];
+            const float4 nl = reinterpret_cast<const float4*>(vec + 128)[u];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int e = 4 * u + 2 * hf;
+              float x0 = __uint_as_float(p1[e]), x1 = __uint_as_float(p1[e + 1]);
+              float y0 = __uint_as_float(p2[e]), y1 = __uint_as_float(p2[e + 1]);
+              const float la0 = hf ? la.z : la.x, la1 = hf ? la.w : la.y;
+              const float lb0 = hf ? lb.z : lb.x, lb1 = hf ? lb.w : lb.y;
+              const float nl0 = hf ? nl.z : nl.x, nl1 = hf ? nl.w : nl.y;
+              if constexpr (decltype(masked)::value) {
+                // Masked entries are exactly 0 (MUFU of -inf).
+                x0 = (e < cm) ? -INFINITY : x0;
+                x1 = (e + 1 < cm) ? -INFINITY : x1;
+                y0 = (e < cm) ? -INFINITY : y0;
+                y1 = (e + 1 < cm) ? -INFINITY : y1;
+                x0 = ex2(fmaf(x0, sl2, -la0));
+                x1 = ex2(fmaf(x1, sl2, -la1));
+                y0 = ex2(fmaf(y0, sl2, -lb0));
+                y1 = ex2(fmaf(y1, sl2, -lb1));
+              } else {
+                const uint64_t tx = fma2(f2(x0, x1), sl2x2, f2(-la0, -la1));
+                const uint64_t ty = fma2(f2(y0, y1), sl2x2, f2(-lb0, -lb1));
+                f2_split(tx, x0, x1);
+                x0 = ex2(x0);
+                x1 = ex2(x1);
+                if (hf) {  // one pair in four on the FMA pipe
+                  f2_split(exp2_poly2(ty), y0, y1);
+                } else {
+                  f2_split(ty, y0, y1);
+                  y0 = ex2(y0);
+                  y1 = ex2(y1);
+                }
+              }
+              y0 *= nl0;
+              y1 *= nl1;
+              p1[e] = __float_as_uint(x0), p1[e + 1] = __float_as_uint(x1);
+              p2[e] = __float_as_uint(y0), p2[e + 1] = __float_as_uint(y1);
+              w[e >> 1] = pack2<BF16>(x0 + y0, x1 + y1);
+            }
+          }
+        };
+        if (__any_sync(0xffffffffu, cm > 0))
+          block(std::true_type{});
+        else
+          block(std::false_type{});
+        tmem_st16(tS1, w);  // this warpgroup's own 32 columns of S_1, read above
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(w_ready);
+      // Phase B: dS_1 = p1 (dP - Delta_1), dS_2 = p2 (dP - Delta_2), 16 bits,
+      // into swizzled shared memory.
+      ok = __all_sync(0xffffffffu, wait_bar(dp_full, i & 1, abort_flag, kRoleSoftmax, i) &&
+                                       wait_bar(ds_free, ((i >> 1) & 1) ^ 1, abort_flag, kRoleSoftmax, i));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dp[32];
+      tmem_ld32(tDP, dp);
+      tmem_ld_wait();
+      reg_fence(dp);
+      const uint32_t row1 = smem_u32(smem + L::OFF_DS + (i & 1) * L::BLK) + kr * 128;
+      const uint32_t row2 = row1 + 2 * L::BLK;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // 8 queries: one 16-byte chunk of each map's row
+        uint32_t d1[4], d2[4];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const float4 da = reinterpret_cast<const float4*>(vec + 192)[2 * u + v];
+          const float4 db = reinterpret_cast<const float4*>(vec + 256)[2 * u + v];
+          const int e = 8 * u + 4 * v;
+          auto f = [](uint32_t x) { return __uint_as_float(x); };
+          d1[2 * v] = pack2<BF16>(f(p1[e]) * (f(dp[e]) - da.x), f(p1[e + 1]) * (f(dp[e + 1]) - da.y));
+          d1[2 * v + 1] = pack2<BF16>(f(p1[e + 2]) * (f(dp[e + 2]) - da.z), f(p1[e + 3]) * (f(dp[e + 3]) - da.w));
+          d2[2 * v] = pack2<BF16>(f(p2[e]) * (f(dp[e]) - db.x), f(p2[e + 1]) * (f(dp[e + 1]) - db.y));
+          d2[2 * v + 1] = pack2<BF16>(f(p2[e + 2]) * (f(dp[e + 2]) - db.z), f(p2[e + 3]) * (f(dp[e + 3]) - db.w));
+        }
+        const uint32_t at = ((4 * g + u) ^ (kr & 7)) << 4;
+        st_shared_v4(row1 + at, d1[0], d1[1], d1[2], d1[3]);
+        st_shared_v4(row2 + at, d2[0], d2[1], d2[2], d2[3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(ds_ready);
+    }
+    // Epilogue: warpgroup 0 writes dK_c = scale * accumulator, warpgroup 1 dV.
+    if (ok && !*abort_flag) {
+      const bool have = n > 0;
+      if (!have || __all_sync(0xffffffffu, wait_bar(mma_done, 0, abort_flag, kRoleSoftmax, n))) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int x = 0; x < (g == 0 ? 4 : DV / 32); ++x) {  // 32 accumulator columns
+          const int c = x >> 1;
+          const int col = g == 0 ? 32 * (x & 1) : 32 * x;  // first column of the tensor
+          uint16_t* dst = g == 0 ? reinterpret_cast<uint16_t*>(a.dk[c]) + b * a.dk_s[c][0] + key * a.dk_s[c][1] +
+                                       hk * a.dk_s[c][2] + col
+                                 : reinterpret_cast<uint16_t*>(a.dv) + b * a.dv_s[0] + key * a.dv_s[1] +
+                                       hk * a.dv_s[2] + col;
+          const int cols = g == 0 ? a.d : a.dv_cols;
+          const float mul = g == 0 ? a.scale : 1.f;
+          uint32_t v[32];
+          if (have) {
+            tmem_ld32(tmem + lane_base + (g == 0 ? L::COL_DK : L::COL_DV) + 32 * x, v);
+            tmem_ld_wait();
+            reg_fence(v);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          }
+          if (key < a.Sk && checked(b < a.B && hk < a.Hk, 512)) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<BF16>(__uint_as_float(v[8 * u + 2 * e]) * mul, __uint_as_float(v[8 * u + 2 * e + 1]) * mul);
+              if (col + 8 * u < cols) reinterpret_cast<uint4*>(dst)[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------- dQ drain (warps 8-11)
+    const int wq = warp & 3;
+    const int tr = wq * 32 + lane;  // TMEM lane = query row of the block
+    const uint32_t tDQ = tmem + (static_cast<uint32_t>(wq * 32) << 16) + L::COL_DQ;
+    for (int u = 0; u < n; ++u) {  // one use of the dQ buffer per map and block
+      if (!__all_sync(0xffffffffu, wait_bar(dq_full, u & 1, abort_flag, kRoleSoftmax, u))) break;
+      tc_fence_after();
+      const int c = u & 1;
+      const int bh = chunk_bh(u), r0 = chunk_row(u & ~1);
+      uint32_t v[2][32];
+      tmem_ld32(tDQ, v[0]);
+      tmem_ld32(tDQ + 32, v[1]);
+      tmem_ld_wait();
+      reg_fence(v[0]);
+      reg_fence(v[1]);
+      tc_fence_before();
+      mbar_arrive(dq_free);
+      if (a.dq_part != nullptr) {
+        if (checked(bh < a.B * a.H && r0 / 128 < a.nqb && kvb < a.nkb, 513)) {
+          float4* dst = reinterpret_cast<float4*>(
+              a.dq_part +
+              (((static_cast<int64_t>(bh) * a.nqb + r0 / 128) * a.nkb + kvb) * 2 + c) * (128 * 64) + tr * 64);
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[8 * p + e] = make_float4(__uint_as_float(v[p][4 * e]), __uint_as_float(v[p][4 * e + 1]),
+                                           __uint_as_float(v[p][4 * e + 2]), __uint_as_float(v[p][4 * e + 3]));
+        }
+      } else {
+        // Two boxes of 32 rows x 32 floats, one after the other through this
+        // warp's 4 KB, in the 128-byte swizzled layout that tmDQ reads: row
+        // r's 16-byte chunk e at r * 128 + ((e ^ (r % 8)) * 16), so a store
+        // phase's eight lanes hit eight different bank groups.
+        uint8_t* buf = smem + L::OFF_DQS + wq * 4096;
+        const uint32_t rbase = smem_u32(buf) + lane * 128;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          if (lane == 0) bulk_wait_read0();  // the reduction that read this buffer last
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            st_shared_v4(rbase + ((e ^ (lane & 7)) << 4), v[p][4 * e], v[p][4 * e + 1], v[p][4 * e + 2],
+                         v[p][4 * e + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int64_t row = c * acc_rows + static_cast<int64_t>(bh) * a.Sq_pad + r0 + 32 * wq;
+            if (checked(row + 32 <= 2 * acc_rows, 514)) tma_reduce_add_2d(&tmDQ, buf, 32 * p, static_cast<int>(row));
+            bulk_commit();
+          }
+        }
+      }
+    }
+    // Let the TMA finish the last reductions before shared memory goes away.
+    if (lane == 0) bulk_wait0();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+}  // namespace fa

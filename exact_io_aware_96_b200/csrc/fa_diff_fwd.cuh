@@ -1,0 +1,481 @@
+// fa_diff_fwd.cuh — differential attention forward for sm_100a (fa_diff_fwd):
+//   P_c = softmax(scale Q_c K_c^T [+ mask]), c = 1, 2
+//   O   = (P_1 - lambda P_2) V,
+// with two query/key projections of head_dim D <= 64 per head, one value
+// projection of width Dv <= 128, and a weight lambda per (batch, row, head)
+// (or broadcast over any of them). Heads of q may share a key/value head.
+//
+// The two maps have row maxima and sums of their own, so the difference can
+// only be taken at the end: O = O_1 / l_1 - lambda O_2 / l_2 with
+// unnormalised O_c = sum_j 2^(x_cj - m_c) v_j. One CTA takes 128 query rows of
+// one (batch, head) and runs both maps side by side, map c where the plain
+// forward has its query tile t = c: while one map's softmax runs, the tensor
+// core works on the other map's products, and V is read from memory and
+// shared memory once for both. The difference is formed in the epilogue from
+// the two accumulators in tensor memory; nothing of either map reaches device
+// memory. For training, O_2 (16 bits) and both logsumexps are written too:
+// with O they give both row terms of the backward.
+//
+// The online softmax, the lazily raised maximum and the exponentials (one
+// pair in four on the FMA pipe where no entry is masked) are those of
+// fa_fwd.cuh.
+//
+// Warp roles (576 threads):
+//   warps 8t + 4c + r  softmax of map t, key half c of every block, TMEM lanes
+//              32r .. 32r + 31, one query row per thread
+//   warp  16   TMA loader: Q_1, Q_2 once, then (K_1, K_2)_j and V_j into rings
+//   warp  17   MMA issuer
+// Tensor memory: [128t, 128t + 128) S_t, then P_t   [256 + t DV, + DV) O_t
+//
+// What bounds it: per 128 x 128 block the products take 4 x 128 x 128 x (64 +
+// DV) flops (1536 tensor cycles at DV = 128) and the softmax 2 x 128 x 128
+// exponentials (2048 MUFU cycles, 1536 with a quarter of them moved to the
+// FMA pipe).
+#pragma once
+
+#include "fa_common.cuh"
+#include "fa_fwd.cuh"
+
+namespace fa {
+
+enum LamKind : int { kLamF16 = 0, kLamBF16 = 1, kLamF32 = 2 };
+
+__device__ __forceinline__ float load_lam(const void* lam, int kind, int64_t at) {
+  if (kind == kLamF32) return static_cast<const float*>(lam)[at];
+  const uint16_t v = static_cast<const uint16_t*>(lam)[at];
+  return kind == kLamBF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+}
+
+struct DiffFwdArgs {
+  void* o;
+  void* o2;  // may be null
+  float* lse;  // fp32 [2][B][H][Sq]
+  int64_t o_s[3], o2_s[3];  // element strides: batch, sequence, head
+  const void* lam;
+  int64_t lam_s[3];  // 0 where lambda is broadcast
+  int lam_kind;
+  const int* k_lens;  // keys of each batch entry (null: Sk for all)
+  int B, H, Hk, Sq, Sk;
+  int dv;  // columns of v and o (<= the kernel's DV)
+  float scale_log2;
+  int causal;
+  int n_qblocks;  // ceil(Sq / 128)
+};
+
+__device__ __forceinline__ int diff_keys(const int* k_lens, int b, int Sk) {
+  return k_lens == nullptr ? Sk : max(0, min(k_lens[b], Sk));
+}
+
+template <int DV>
+struct DiffFwdLayout {
+  static constexpr int kThreads = 576;
+  static constexpr int kLoaderWarp = 16;
+  static constexpr int kMmaWarp = 17;
+  static constexpr int BLK = 128 * 128;  // one 128-row x 128-byte block
+  static constexpr int VB = DV / 64;     // column blocks of V
+  static constexpr int KS = 3;           // stages of (K_1, K_2)
+  static constexpr int VS = DV == 128 ? 2 : 3;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * BLK;
+  static constexpr int OFF_V = OFF_K + KS * 2 * BLK;
+  static constexpr int OFF_PMAX = OFF_V + VS * VB * BLK;      // [parity][map][half][row]
+  static constexpr int OFF_LSUM = OFF_PMAX + 2 * 2 * 2 * 128 * 4;  // [map][half][row]
+  static constexpr int OFF_M = OFF_LSUM + 2 * 2 * 128 * 4;    // [map][row]
+  static constexpr int OFF_BAR = OFF_M + 2 * 128 * 4;
+  // q_full, k_full/k_empty[KS], v_full/v_empty[VS], s_full[2], p_full[2], o_final[2], drain
+  static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 6 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int SMEM_ALLOC = BYTES + 1024;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int OBASE = 256;
+};
+
+template <int DV, bool BF16>
+__global__ void __launch_bounds__(576, 1)
+    fa_diff_fwd_kernel(const __grid_constant__ CUtensorMap tmQ1, const __grid_constant__ CUtensorMap tmQ2,
+                       const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmK2,
+                       const __grid_constant__ CUtensorMap tmV, const DiffFwdArgs a) {
+  using L = DiffFwdLayout<DV>;
+  using namespace sm100;
+  constexpr int KS = L::KS, VS = L::VS;
+  static_assert(L::SMEM_ALLOC <= 232448, "smem budget");
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* k_empty = k_full + KS;
+  uint64_t* v_full = k_empty + KS;
+  uint64_t* v_empty = v_full + VS;
+  uint64_t* s_full = v_empty + VS;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_final = p_full + 2;
+  uint64_t* drain = o_final + 2;
+  float* pmax = reinterpret_cast<float*>(smem + L::OFF_PMAX);
+  float* lsum = reinterpret_cast<float*>(smem + L::OFF_LSUM);
+  float* msm = reinterpret_cast<float*>(smem + L::OFF_M);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // Grid order as the plain forward's: with a causal mask rank-major over
+  // (b, h), the last query blocks (the most key blocks) first; without one
+  // head-major, so that the running CTAs share a few heads' K and V in L2.
+  const int hb_count = a.H * a.B;
+  const int rank = a.causal ? static_cast<int>(blockIdx.x) / hb_count : static_cast<int>(blockIdx.x) % a.n_qblocks;
+  const int hb = a.causal ? static_cast<int>(blockIdx.x) % hb_count : static_cast<int>(blockIdx.x) / a.n_qblocks;
+  const int h = hb % a.H;
+  const int b = hb / a.H;
+  const int hk = h / (a.H / a.Hk);
+  const int q0 = (a.causal ? a.n_qblocks - 1 - rank : rank) * 128;
+  const int sk = diff_keys(a.k_lens, b, a.Sk);
+  const int n = fwd_kv_blocks(q0, a.Sq, sk, a.causal);
+  checked(q0 < a.Sq && b < a.B && hk < a.Hk, 401);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 8);  // one arrival per softmax warp of the map
+      mbar_init(&o_final[t], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == L::kLoaderWarp && lane == 0) {
+    prefetch_tmap(&tmQ1);
+    prefetch_tmap(&tmQ2);
+    prefetch_tmap(&tmK1);
+    prefetch_tmap(&tmK2);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == L::kMmaWarp) {
+    tmem_alloc(tmem_slot, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == L::kLoaderWarp) {
+    // ------------------------------------------------------------ loader
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(q_full, 2 * L::BLK);
+      tma_load_4d(smem + L::OFF_Q, &tmQ1, q_full, 0, q0, h, b);
+      tma_load_4d(smem + L::OFF_Q + L::BLK, &tmQ2, q_full, 0, q0, h, b);
+      int nk = 0, nv = 0;  // loads issued
+      for (int j = 0; j < n; ++j) {
+        const int ks = j % KS, vs = j % VS;
+        checked(j * 128 < sk, 402);
+        if (!wait_bar(&k_empty[ks], ((j / KS) & 1) ^ 1, abort_flag, kRoleLoader, j)) break;
+        mbar_arrive_expect_tx(&k_full[ks], 2 * L::BLK);
+        tma_load_4d(smem + L::OFF_K + ks * 2 * L::BLK, &tmK1, &k_full[ks], 0, j * 128, hk, b);
+        tma_load_4d(smem + L::OFF_K + (ks * 2 + 1) * L::BLK, &tmK2, &k_full[ks], 0, j * 128, hk, b);
+        ++nk;
+        if (!wait_bar(&v_empty[vs], ((j / VS) & 1) ^ 1, abort_flag, kRoleLoader, j)) break;
+        mbar_arrive_expect_tx(&v_full[vs], L::VB * L::BLK);
+        for (int vb = 0; vb < L::VB; ++vb)
+          tma_load_4d(smem + L::OFF_V + (vs * L::VB + vb) * L::BLK, &tmV, &v_full[vs], vb * 64, j * 128, hk, b);
+        ++nv;
+      }
+      if (*abort_flag) {
+        // Let the copies already issued land before the CTA exits.
+        drain_wait(q_full, 0);
+        for (int j = max(0, nk - KS); j < nk; ++j) drain_wait(&k_full[j % KS], (j / KS) & 1);
+        for (int j = max(0, nv - VS); j < nv; ++j) drain_wait(&v_full[j % VS], (j / VS) & 1);
+      }
+    }
+  } else if (warp == L::kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (n > 0) {
+      auto wait = [&](uint64_t* bar, uint32_t parity, int iter) {
+        return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, kRoleMma, iter));
+      };
+      constexpr uint32_t idS = idesc_f16(BF16, 128, 128, 0, 0);
+      constexpr uint32_t idO = idesc_f16(BF16, 128, DV, 0, 1);
+      const uint32_t sQ = smem_u32(smem + L::OFF_Q);
+      const uint32_t sK = smem_u32(smem + L::OFF_K);
+      const uint32_t sV = smem_u32(smem + L::OFF_V);
+      auto issue_S = [&](int t, int ks) {
+        const uint64_t qd = desc_sw128(sQ + t * L::BLK, 16, 1024);
+        const uint64_t kd = desc_sw128(sK + (ks * 2 + t) * L::BLK, 16, 1024);
+        uint64_t ad[4], bd[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          ad[u] = desc_add(qd, u * 32);
+          bd[u] = desc_add(kd, u * 32);
+        }
+        mma_ss_x4(tmem + 128 * t, ad, bd, idS, 0);
+      };
+      auto issue_PV = [&](int t, int vs, int acc) {
+        const uint64_t vd = desc_sw128(sV + vs * L::VB * L::BLK, L::BLK, 1024);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pa[4];
+          uint64_t vb[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            pa[u] = tmem + 128 * t + 64 * hf + u * 8;
+            vb[u] = desc_add(vd, (4 * hf + u) * 2048);
+          }
+          mma_ts_x4(tmem + L::OBASE + t * DV, pa, vb, idO, (acc || hf > 0) ? 1u : 0u);
+        }
+      };
+      bool ok = wait(q_full, 0, -1) && wait(&k_full[0], 0, 0);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
+          issue_S(t, 0);
+          mma_commit_w(&s_full[t]);
+        }
+        mma_commit_w(&k_empty[0]);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const int vs = j % VS;
+        const int jn = j + 1, ksn = jn % KS;
+        if (!(ok = wait(&v_full[vs], (j / VS) & 1, j))) break;
+        if (jn < n && !(ok = wait(&k_full[ksn], (jn / KS) & 1, jn))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !(ok = wait(&p_full[t], j & 1, j))) break;
+          tc_fence_after();
+          issue_PV(t, vs, j > 0);
+          if (j == n - 1) mma_commit_w(&o_final[t]);
+          if (t == 1) mma_commit_w(&v_empty[vs]);
+          if (jn < n) {
+            issue_S(t, ksn);
+            mma_commit_w(&s_full[t]);
+            if (t == 1) mma_commit_w(&k_empty[ksn]);
+          }
+        }
+      }
+      // Wait for every MMA this warp issued before TMEM is released.
+      mma_commit_w(drain);
+      drain_wait(drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------- softmax / epilogue
+    const int t = warp >> 3;            // map
+    const int c = (warp >> 2) & 1;      // key half of every block
+    const int quarter = warp & 3;       // TMEM lane quarter
+    const int r = quarter * 32 + lane;  // row within the tile
+    const int row = q0 + r;
+    const int pair_bar = 1 + t * 4 + quarter;  // named barrier of the two warps that share these rows
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_base + 128 * t + 64 * c;
+    const uint32_t tO = tmem + lane_base + L::OBASE + t * DV + c * (DV / 2);  // the half this warp rescales
+    const float sl2 = a.scale_log2;
+    const int off = sk - a.Sq;
+    float m = -INFINITY;  // running max of x = s * scale * log2(e), the same in both halves
+    float l = 0.f;        // this half's running sum of 2^(x - m)
+    bool ok = true;
+
+    for (int j = 0; j < n; ++j) {
+      // `ok` false here: a wait of the previous block ran out; this warp goes
+      // straight to the pair barrier, which then ends both warps.
+      const bool ready = ok && __all_sync(0xffffffffu, wait_bar(&s_full[t], j & 1, abort_flag, kRoleSoftmax, j));
+      const int k0 = j * 128 + 64 * c;  // first key of this half
+      const bool masked = k0 + 64 > sk || (a.causal && k0 + 63 > q0 + off);
+      int lim = sk - 1 - k0;  // last allowed column of this half
+      if (a.causal) lim = min(lim, row + off - k0);
+      float* slot = pmax + (((j & 1) * 2 + t) * 2) * 128;
+      float pm = -INFINITY;
+      if (ready) {
+        tc_fence_after();
+        uint32_t rr[2][32];
+        tmem_ld32(tS, rr[0]);
+        tmem_ld32(tS + 32, rr[1]);
+        tmem_ld_wait();
+        reg_fence(rr[0]);
+        reg_fence(rr[1]);
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              rr[q][i] = (32 * q + i <= lim) ? rr[q][i] : __float_as_uint(-INFINITY);
+        }
+        auto xf = [&](int i) { return __uint_as_float(rr[i >> 5][i & 31]); };
+        float mx0 = max3(xf(0), xf(1), xf(2)), mx1 = max3(xf(3), xf(4), xf(5));
+        float mx2 = max3(xf(6), xf(7), xf(8)), mx3 = max3(xf(9), xf(10), xf(11));
+#pragma unroll
+        for (int i = 12; i < 60; i += 8) {
+          mx0 = max3(mx0, xf(i), xf(i + 1));
+          mx1 = max3(mx1, xf(i + 2), xf(i + 3));
+          mx2 = max3(mx2, xf(i + 4), xf(i + 5));
+          mx3 = max3(mx3, xf(i + 6), xf(i + 7));
+        }
+        mx0 = max3(mx0, xf(60), xf(61));
+        mx1 = max3(mx1, xf(62), xf(63));
+        pm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        // Written again in block j + 2, after the partner has passed the
+        // barrier of block j + 1, i.e. after it has read this value.
+        slot[c * 128 + r] = pm;
+      }
+      if (!named_bar_and(pair_bar, 64, ready)) {
+        ok = false;
+        break;
+      }
+      const float m_blk = fmaxf(pm, slot[(c ^ 1) * 128 + r]) * sl2;
+      const bool raise = m_blk > m + 8.0f;
+      float alpha = 1.f;
+      if (raise) {
+        alpha = ex2(m - m_blk);  // 0 when m was -inf
+        m = m_blk;
+      }
+      l *= alpha;
+      // S_t(j) was issued after P_t(j-1) V_{j-1}, so s_full covers both and
+      // O_t may be rescaled now.
+      if (j > 0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll 1
+        for (int q = 0; q < DV / 64; ++q) {
+          uint32_t ov[32];
+          tmem_ld32(tO + 32 * q, ov);
+          tmem_ld_wait();
+          reg_fence(ov);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+          tmem_st32(tO + 32 * q, ov);
+        }
+      }
+      const float mu = (m == -INFINITY) ? 0.f : m;
+      const uint64_t sl2x2 = f2(sl2, sl2);
+      const uint64_t negmu2 = f2(-mu, -mu);
+      uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
+      // S is read again 32 columns at a time; P of columns 0-31 goes to
+      // columns 0-15, P of 32-63 to 16-31, each after the S values under it
+      // have been read.
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t sv[32];
+        tmem_ld32(tS + 32 * q, sv);
+        tmem_ld_wait();
+        reg_fence(sv);
+        uint32_t pw[16];
+        if (masked)
+          fwd_exp32<BF16, true>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw);
+        else
+          fwd_exp32<BF16, false>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw);
+        tmem_st16(tS + 16 * q, pw);
+      }
+      {
+        const uint64_t acc = add2(acc0, acc1);
+        float a0, a1;
+        f2_split(acc, a0, a1);
+        l += a0 + a1;
+      }
+      if (t == 0 && a.k_lens != nullptr && j == n - 1 && (j + 1) * 128 > sk) {
+        // V rows past this sequence's last key (whatever a cache holds there)
+        // become zeros before P V reads them: their P is 0, but 0 x inf is
+        // not. Both products read V after map 1's warps have arrived below.
+        if (!__all_sync(0xffffffffu,
+                        wait_bar(&v_full[j % VS], (j / VS) & 1, abort_flag, kRoleSoftmax, j))) {
+          ok = false;  // the epilogue's barrier ends every warp
+          continue;
+        }
+        uint8_t* vt = smem + L::OFF_V + (j % VS) * L::VB * L::BLK;
+        for (int i = threadIdx.x; i < L::VB * 128 * 8; i += 256) {  // 16-byte chunks, 8 to a row
+          const int vr = (i >> 3) & 127;
+          if (j * 128 + vr >= sk)
+            st_shared_v4(smem_u32(vt + (i >> 10) * L::BLK + vr * 128 + (i & 7) * 16), 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+
+    // Epilogue: all 16 warps meet with both maps' sums; each warpgroup then
+    // writes a quarter of the columns from both accumulators.
+    lsum[(t * 2 + c) * 128 + r] = l;
+    if (c == 0) msm[t * 128 + r] = m;
+    constexpr int kAllBar = 9;
+    bool go = named_bar_and(kAllBar, 512, ok && !*abort_flag);
+    const int wg = warp >> 2;
+    constexpr int NC = DV / 4;  // columns of one warpgroup
+    const int cb = wg * NC;
+    if (go && n > 0) {
+      go = __all_sync(0xffffffffu, wait_bar(&o_final[0], 0, abort_flag, kRoleSoftmax, n) &&
+                                       wait_bar(&o_final[1], 0, abort_flag, kRoleSoftmax, n));
+      tc_fence_after();
+    }
+    if (go) {
+      const bool valid = row < a.Sq;
+      const float l1 = lsum[r] + lsum[128 + r], l2 = lsum[256 + r] + lsum[384 + r];
+      const float m1 = msm[r], m2 = msm[128 + r];
+      const bool has = sk > 0 && (!a.causal || row + off >= 0);  // some key is allowed (the same in both maps)
+      const float lam = valid && has ? load_lam(a.lam, a.lam_kind, b * a.lam_s[0] + row * a.lam_s[1] + h * a.lam_s[2])
+                                     : 0.f;
+      const float inv1 = has ? 1.f / l1 : 0.f, inv2 = has ? 1.f / l2 : 0.f;
+      uint32_t o1[NC], o2[NC];
+      if (n > 0) {
+        const uint32_t t1 = tmem + lane_base + L::OBASE + cb;
+        if constexpr (NC == 32) {
+          tmem_ld32(t1, o1);
+          tmem_ld32(t1 + DV, o2);
+        } else {
+          tmem_ld16(t1, o1);
+          tmem_ld16(t1 + DV, o2);
+        }
+        tmem_ld_wait();
+        reg_fence(o1);
+        reg_fence(o2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) o1[i] = o2[i] = 0u;
+      }
+      if (valid && checked(b < a.B && h < a.H && row < a.Sq, 403)) {
+        uint16_t* orow = reinterpret_cast<uint16_t*>(a.o) + b * a.o_s[0] + row * a.o_s[1] + h * a.o_s[2] + cb;
+        uint16_t* orow2 = reinterpret_cast<uint16_t*>(a.o2) + b * a.o2_s[0] + row * a.o2_s[1] + h * a.o2_s[2] + cb;
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) {
+          uint32_t w[4], w2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 8 * i + 2 * e;
+            const float y0 = has ? __uint_as_float(o2[x]) * inv2 : 0.f;
+            const float y1 = has ? __uint_as_float(o2[x + 1]) * inv2 : 0.f;
+            const float x0 = has ? __uint_as_float(o1[x]) * inv1 : 0.f;
+            const float x1 = has ? __uint_as_float(o1[x + 1]) * inv1 : 0.f;
+            w[e] = pack2<BF16>(x0 - lam * y0, x1 - lam * y1);
+            w2[e] = pack2<BF16>(y0, y1);
+          }
+          if (cb + 8 * i < a.dv) {
+            reinterpret_cast<uint4*>(orow)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (a.o2 != nullptr) reinterpret_cast<uint4*>(orow2)[i] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          }
+        }
+        if (wg < 2) {  // warpgroup 0 writes map 1's LSE, warpgroup 1 map 2's
+          const float lm = wg ? m2 : m1, ll = wg ? l2 : l1;
+          a.lse[((static_cast<int64_t>(wg) * a.B + b) * a.H + h) * a.Sq + row] =
+              has ? (lm + __log2f(ll)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+}  // namespace fa

@@ -9,6 +9,7 @@ receives only pointers and those sizes) and launch on q's device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -33,7 +34,10 @@ FA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_fp8_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_noalloc",
             "fa_fwd_workspace_size", "fa_fwd_workspace_size_ex", "fa_fwd_split_plan",
             "fa_bwd_workspace_size", "fa_bwd_workspace_size_ex", "fa_selftest_wait_timeout",
+            "fa_diff_fwd", "fa_diff_fwd_workspace_size", "fa_diff_bwd", "fa_diff_bwd_workspace_size", "fa_rotary",
             "fa_last_device_status", "fa_strerror", "fa_version")
+FA_LAMBDA_FP32 = 2
+FA_ROTARY_MAX_AXES = 8
 
 
 class FaTensor(ctypes.Structure):
@@ -68,6 +72,43 @@ class BwdParams(ctypes.Structure):
                 ("D", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("deterministic", ctypes.c_int)]
+
+
+class DiffLambda(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("extent_b", ctypes.c_int), ("extent_s", ctypes.c_int),
+                ("extent_h", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class DiffFwdParams(ctypes.Structure):
+    _fields_ = [("q", FaTensor * 2), ("k", FaTensor * 2), ("v", FaTensor), ("lam", DiffLambda),
+                ("k_lens", ctypes.c_void_p), ("o", FaTensor), ("o2", FaTensor), ("lse", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("Sq", ctypes.c_int),
+                ("Sk", ctypes.c_int), ("D", ctypes.c_int), ("Dv", ctypes.c_int), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class DiffBwdParams(ctypes.Structure):
+    _fields_ = [("q", FaTensor * 2), ("k", FaTensor * 2), ("v", FaTensor), ("o", FaTensor), ("o2", FaTensor),
+                ("dO", FaTensor), ("lse", ctypes.c_void_p), ("lam", DiffLambda),
+                ("dq", FaTensor * 2), ("dk", FaTensor * 2), ("dv", FaTensor), ("dlam", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("Sq", ctypes.c_int),
+                ("Sk", ctypes.c_int), ("D", ctypes.c_int), ("Dv", ctypes.c_int), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("deterministic", ctypes.c_int)]
+
+
+class RotaryParams(ctypes.Structure):
+    _fields_ = [("q", FaTensor), ("k", FaTensor), ("q_out", FaTensor), ("k_out", FaTensor),
+                ("positions", ctypes.c_void_p), ("pos_stride_axis", ctypes.c_int64),
+                ("pos_stride_b", ctypes.c_int64), ("pos_stride_s", ctypes.c_int64), ("pos_int64", ctypes.c_int),
+                ("inv_freq", ctypes.c_void_p), ("inv_freq_fp64", ctypes.c_int), ("axes", ctypes.c_int),
+                ("sections", ctypes.c_int * FA_ROTARY_MAX_AXES),
+                ("B", ctypes.c_int), ("S", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("D", ctypes.c_int), ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -120,6 +161,16 @@ def lib():
         L.fa_bwd_workspace_size.restype = sz
         L.fa_bwd_workspace_size_ex.argtypes = [i, i, i, i, i, i]
         L.fa_bwd_workspace_size_ex.restype = sz
+        L.fa_diff_fwd.argtypes = [ctypes.POINTER(DiffFwdParams), vp]
+        L.fa_diff_fwd.restype = i
+        L.fa_diff_fwd_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+        L.fa_diff_fwd_workspace_size.restype = sz
+        L.fa_diff_bwd.argtypes = [ctypes.POINTER(DiffBwdParams), vp]
+        L.fa_diff_bwd.restype = i
+        L.fa_diff_bwd_workspace_size.argtypes = [i, i, i, i, i]
+        L.fa_diff_bwd_workspace_size.restype = sz
+        L.fa_rotary.argtypes = [ctypes.POINTER(RotaryParams), vp]
+        L.fa_rotary.restype = i
         L.fa_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
         L.fa_selftest_wait_timeout.restype = i
         L.fa_last_device_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
@@ -173,6 +224,26 @@ def fa_bwd_workspace_size(B, H, Sq, D) -> int:
 
 def fa_bwd_workspace_size_ex(B, H, Sq, Sk, D, deterministic) -> int:
     return lib().fa_bwd_workspace_size_ex(B, H, Sq, Sk, D, deterministic)
+
+
+def fa_diff_fwd(params: DiffFwdParams, stream=0) -> int:
+    return lib().fa_diff_fwd(ctypes.byref(params), stream)
+
+
+def fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal) -> int:
+    return lib().fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal)
+
+
+def fa_diff_bwd(params: DiffBwdParams, stream=0) -> int:
+    return lib().fa_diff_bwd(ctypes.byref(params), stream)
+
+
+def fa_diff_bwd_workspace_size(B, H, Sq, Sk, deterministic) -> int:
+    return lib().fa_diff_bwd_workspace_size(B, H, Sq, Sk, deterministic)
+
+
+def fa_rotary(params: RotaryParams, stream=0) -> int:
+    return lib().fa_rotary(ctypes.byref(params), stream)
 
 
 def fa_selftest_wait_timeout(limit_us, stream=0) -> int:
@@ -418,3 +489,247 @@ def backward(q, k, v, o, lse, do, causal=False, scale=None, dq=None, dk=None, dv
     if st != FA_OK:
         raise FaError(st, "fa_bwd_ex")
     return dq, dk, dv
+
+
+# ------------------------------------- differential attention, rotary positions
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The raw handle of the launch stream on `dev`. A stream given by the
+    caller is made torch's current one meanwhile, so that what the helper
+    allocates belongs to the stream that uses it."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = _stream(stream)
+            stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, q on {dev}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _pair_view(t: torch.Tensor):
+    """The two maps' [B, S, H, D] views of a [B, S, H, 2, D] tensor."""
+    sb, ss, sh, sc, _ = t.stride()
+    at = t.data_ptr()
+    return (FaTensor * 2)(FaTensor(at, sb, ss, sh), FaTensor(at + 2 * sc, sb, ss, sh))
+
+
+def _diff_dims(q, k, v):
+    if q.dim() != 5 or k.dim() != 5 or v.dim() != 4 or q.shape[3] != 2 or k.shape[3] != 2:
+        raise ValueError("expected q [B, Sq, H, 2, D], k [B, Sk, Hk, 2, D] and v [B, Sk, Hk, Dv]")
+    B, Sq, H, _, D = q.shape
+    Sk, Hk, Dv = v.shape[1:]
+    dt = _dtype_code(q)
+    _expect("k", k, (B, Sk, Hk, 2, D), q.dtype, q.device)
+    _expect("v", v, (B, Sk, Hk, Dv), q.dtype, q.device)
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} query heads cannot share {Hk} key heads evenly")
+    if not q.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
+    return B, Sq, H, D, Sk, Hk, Dv, dt
+
+
+def _last_axis(**tensors) -> None:
+    for name, t in tensors.items():
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name}: the last axis must be contiguous")
+
+
+def _lambda(lam, B, Sq, H, q) -> DiffLambda:
+    if not isinstance(lam, torch.Tensor) or lam.dim() > 3:
+        raise ValueError("lam must be a tensor that broadcasts to [B, Sq, H]")
+    ext = (1,) * (3 - lam.dim()) + tuple(lam.shape)
+    if any(e != 1 and e != n for e, n in zip(ext, (B, Sq, H))):
+        raise ValueError(f"lam: {tuple(lam.shape)} does not broadcast to [{B}, {Sq}, {H}]")
+    if lam.dtype not in (torch.float32, q.dtype):
+        raise TypeError(f"lam: expected float32 or {q.dtype}, got {lam.dtype}")
+    if lam.device != q.device:
+        raise ValueError(f"lam is on {lam.device}, q on {q.device}")
+    st = (0,) * (3 - lam.dim()) + tuple(lam.stride())
+    return DiffLambda(lam.data_ptr(), *st, *ext, FA_LAMBDA_FP32 if lam.dtype == torch.float32 else _DT[lam.dtype])
+
+
+def _diff_lse(lse, B, H, Sq, dev):
+    _expect("lse", lse, (2, B, H, Sq), torch.float32, dev)
+    if not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [2, B, H, Sq] tensor")
+
+
+def _ws_bytes(workspace, dev) -> int:
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous buffer on {dev}")
+    return workspace.numel() * workspace.element_size()
+
+
+def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=False, out=None, out2=None, lse=None,
+                 workspace=None, stream=None):
+    """(O, LSE, O2) of differential attention,
+    O = (softmax(scale q_1 k_1^T) - lam softmax(scale q_2 k_2^T)) v.
+
+    q [B, Sq, H, 2, D], k [B, Sk, Hk, 2, D] and v [B, Sk, Hk, Dv] are CUDA
+    tensors (strided views allowed), D <= 64, Dv <= 128; Hk divides H. lam
+    (float32 or q's dtype) broadcasts to [B, Sq, H]. k_lens, int32 [B]: batch
+    entry b attends to its first k_lens[b] keys, and the causal mask aligns to
+    that end. LSE is fp32 [2, B, H, Sq]. O2 = softmax(scale q_2 k_2^T) v is
+    written if need_o2 or out2 asks for it (diff_backward needs it), else None."""
+    B, Sq, H, D, Sk, Hk, Dv, dt = _diff_dims(q, k, v)
+    dev = q.device
+    lp = _lambda(lam, B, Sq, H, q)
+    if scale is None:
+        scale = D ** -0.5
+    if k_lens is not None:
+        _expect("k_lens", k_lens, (B,), torch.int32, dev)
+        if not k_lens.is_contiguous():
+            raise ValueError("k_lens must be contiguous")
+    with _on(dev, stream) as raw:
+        if out is None:
+            out = torch.empty((B, Sq, H, Dv), dtype=q.dtype, device=dev)
+        if out2 is None and need_o2:
+            out2 = torch.empty((B, Sq, H, Dv), dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((2, B, H, Sq), dtype=torch.float32, device=dev)
+        _expect("out", out, (B, Sq, H, Dv), q.dtype, dev)
+        if out2 is not None:
+            _expect("out2", out2, (B, Sq, H, Dv), q.dtype, dev)
+            _last_axis(out2=out2)
+        _diff_lse(lse, B, H, Sq, dev)
+        _last_axis(q=q, k=k, v=v, out=out)
+        if workspace is None:
+            n = fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, int(bool(causal)))
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        p = DiffFwdParams(_pair_view(q), _pair_view(k), _view(v), lp,
+                          k_lens.data_ptr() if k_lens is not None else None, _view(out),
+                          _view(out2) if out2 is not None else FaTensor(), lse.data_ptr(),
+                          B, H, Hk, Sq, Sk, D, Dv, float(scale), int(bool(causal)), dt,
+                          workspace.data_ptr() if workspace is not None else None,
+                          _ws_bytes(workspace, dev) if workspace is not None else 0)
+        st = fa_diff_fwd(p, raw)
+    if st != FA_OK:
+        raise FaError(st, "fa_diff_fwd")
+    return out, lse, out2
+
+
+def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=None, dk=None, dv=None, dlam=None,
+                  workspace=None, stream=None, deterministic=False):
+    """(dQ, dK, dV, dLam) of L = sum(dO * O) for O of diff_forward, whose o, o2
+    and lse it takes. dLam has lam's shape and dtype: the gradient is summed
+    over the axes lam is broadcast over. ``deterministic=True`` sums dQ in a
+    fixed order (dK, dV and dLam always are)."""
+    B, Sq, H, D, Sk, Hk, Dv, dt = _diff_dims(q, k, v)
+    dev = q.device
+    lp = _lambda(lam, B, Sq, H, q)
+    for name, t in (("o", o), ("o2", o2), ("do", do)):
+        _expect(name, t, (B, Sq, H, Dv), q.dtype, dev)
+    _diff_lse(lse, B, H, Sq, dev)
+    if scale is None:
+        scale = D ** -0.5
+    with _on(dev, stream) as raw:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else dk
+        dv = torch.empty(v.shape, dtype=q.dtype, device=dev) if dv is None else dv
+        dlam = torch.empty(lam.shape, dtype=lam.dtype, device=dev) if dlam is None else dlam
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dlam", dlam, lam)):
+            _expect(name, t, like.shape, like.dtype, dev)
+        if not dlam.is_contiguous():
+            raise ValueError("dlam must be contiguous")
+        _last_axis(q=q, k=k, v=v, o=o, o2=o2, do=do, dq=dq, dk=dk, dv=dv)
+        if workspace is None:
+            n = fa_diff_bwd_workspace_size(B, H, Sq, Sk, int(bool(deterministic)))
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        p = DiffBwdParams(_pair_view(q), _pair_view(k), _view(v), _view(o), _view(o2), _view(do), lse.data_ptr(), lp,
+                          _pair_view(dq), _pair_view(dk), _view(dv), dlam.data_ptr(),
+                          B, H, Hk, Sq, Sk, D, Dv, float(scale), int(bool(causal)), dt,
+                          workspace.data_ptr(), _ws_bytes(workspace, dev), int(bool(deterministic)))
+        st = fa_diff_bwd(p, raw)
+    if st != FA_OK:
+        raise FaError(st, "fa_diff_bwd")
+    return dq, dk, dv, dlam
+
+
+def rotary_inv_freq(sections, base=10000.0, per_axis=False, device="cuda") -> torch.Tensor:
+    """fp64 [R] frequencies base^(-j / R) of R = sum(sections) pairs; with
+    per_axis every axis has a ladder of its own, base^(-j / sections[axis])."""
+    counts = list(sections) if per_axis else [sum(sections)]
+    return torch.tensor([float(base) ** (-j / n) for n in counts for j in range(n)], dtype=torch.float64,
+                        device=device)
+
+
+def _rotary_view(name: str, t: torch.Tensor) -> FaTensor:
+    """[B, S, H, D], or [B, S, H, 2, D] with the two maps as neighbouring heads."""
+    if t.dim() == 5:
+        try:
+            t = t.view(t.shape[0], t.shape[1], -1, t.shape[4])
+        except RuntimeError:
+            raise ValueError(f"{name}: the head axes of [B, S, H, 2, D] must be one run of heads") from None
+    return _view(t)
+
+
+def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
+           stream=None):
+    """(q, k) with rotary positions of one or more axes applied: R pairs of
+    columns of every head turn by positions[axis] * inv_freq[pair].
+
+    q and k (or None) are fp16/bf16 CUDA tensors [B, S, heads, D] (strided views
+    allowed), or [B, S, H, 2, D] as differential attention takes them. positions
+    is int32 or int64 [axes, B, S] ([B, S] for one axis; expanded axes allowed),
+    inv_freq fp32 or fp64 [R]; sections gives the pairs of each axis (default:
+    all on the only axis). Pairs are columns (j, j + R), or (2j, 2j + 1) if
+    interleaved; columns from 2R on are copied. inverse turns back: it is also
+    the gradient. out_q may be q and out_k may be k (in place)."""
+    dt = _dtype_code(q)
+    dev = q.device
+    if q.dim() not in (4, 5) or (k is not None and k.dim() not in (4, 5)):
+        raise ValueError("q and k must be [B, S, H, D] or [B, S, H, 2, D] tensors")
+    B, S, D = q.shape[0], q.shape[1], q.shape[-1]
+    heads = [0, 0]
+    for i, (name, t) in enumerate((("q", q), ("k", k))):
+        if t is None:
+            continue
+        _expect(name, t, (B, S, *t.shape[2:-1], D), q.dtype, dev)
+        heads[i] = t.shape[2] * (t.shape[3] if t.dim() == 5 else 1)
+    if positions.dim() == 2:
+        positions = positions[None]
+    if positions.dim() != 3 or tuple(positions.shape[1:]) != (B, S):
+        raise ValueError(f"positions: expected [axes, {B}, {S}], got {tuple(positions.shape)}")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"positions: expected int32 or int64, got {positions.dtype}")
+    if inv_freq.dtype not in (torch.float32, torch.float64):
+        raise TypeError(f"inv_freq: expected float32 or float64, got {inv_freq.dtype}")
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous [pairs] tensor")
+    for name, t in (("positions", positions), ("inv_freq", inv_freq)):
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+    axes = positions.shape[0]
+    sections = (inv_freq.numel(),) if sections is None else tuple(int(n) for n in sections)
+    if len(sections) != axes or not 1 <= axes <= FA_ROTARY_MAX_AXES:
+        raise ValueError(f"sections: expected one entry for each of 1 to {FA_ROTARY_MAX_AXES} axes, got "
+                         f"{len(sections)} for {axes}")
+    if sum(sections) != inv_freq.numel() or min(sections) < 0:
+        raise ValueError(f"sections {sections} do not add up to inv_freq's {inv_freq.numel()} pairs")
+    if 2 * sum(sections) > D:
+        raise ValueError(f"{sum(sections)} pairs do not fit into {D} columns")
+    with _on(dev, stream) as raw:
+        views = [_rotary_view("q", q), _rotary_view("k", k) if k is not None else FaTensor()]
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev) if out_q is None else out_q
+        _expect("out_q", out_q, q.shape, q.dtype, dev)
+        views.append(_rotary_view("out_q", out_q))
+        if k is not None:
+            out_k = torch.empty(k.shape, dtype=q.dtype, device=dev) if out_k is None else out_k
+            _expect("out_k", out_k, k.shape, q.dtype, dev)
+            views.append(_rotary_view("out_k", out_k))
+        elif out_k is not None:
+            raise ValueError("out_k without k")
+        else:
+            views.append(FaTensor())
+        p = RotaryParams(*views, positions.data_ptr(), *positions.stride(), int(positions.dtype == torch.int64),
+                         inv_freq.data_ptr(), int(inv_freq.dtype == torch.float64), axes,
+                         (ctypes.c_int * FA_ROTARY_MAX_AXES)(*sections), B, S, heads[0], heads[1], D,
+                         int(bool(interleaved)), int(bool(inverse)), dt)
+        st = fa_rotary(p, raw)
+    if st != FA_OK:
+        raise FaError(st, "fa_rotary")
+    return out_q, out_k

@@ -295,6 +295,119 @@ size_t fa_bwd_workspace_size(int B, int H, int Sq, int D);
    than 0 or 1, or on overflow. */
 size_t fa_bwd_workspace_size_ex(int B, int H, int Sq, int Sk, int D, int deterministic);
 
+/* ------------------------------------------------ differential attention
+   With two query/key projections per head, one value projection and a
+   learned weight lambda:
+       P_c = softmax(scale * Q_c K_c^T [+ causal mask]),  c = 1, 2
+       O = (P_1 - lambda P_2) V.
+   Layout: q[c] [B, Sq, H, D], k[c] [B, Sk, Hk, D], v [B, Sk, Hk, Dv], o and o2
+   [B, Sq, H, Dv]: strided views as in fa_fwd_ex, so q[0], q[1] may be the two
+   slices of one [B, Sq, H, 2, D] tensor. An axis longer than 1 may not have
+   stride 0. Query head h reads key/value head h / (H / Hk); Hk divides H.
+   head_dim: D a multiple of 8 in [8, 64], Dv a multiple of 8 in [8, 128];
+   others are FA_ERR_UNSUPPORTED. dtype, scale, causal mask (bottom-right
+   aligned), alignment, ownership, asynchrony and errors as for fa_fwd_ex;
+   2 * B * H * Sq (rounded up to 128) below 2^31. */
+
+/* lambda: one value per (batch, query row, head), or one for all of an axis
+   whose extent is 1 (its stride is then not read). dtype: FA_LAMBDA_FP32, or
+   the call's dtype (FA_FP16 / FA_BF16); strides in elements. */
+#define FA_LAMBDA_FP32 2
+typedef struct {
+  const void* ptr;
+  int64_t stride_b, stride_s, stride_h;
+  int extent_b, extent_s, extent_h; /* 1, or B, Sq, H */
+  int dtype;
+} fa_diff_lambda;
+
+typedef struct {
+  fa_tensor q[2], k[2], v; /* read */
+  fa_diff_lambda lambda;   /* read */
+  const int* k_lens;       /* read; NULL, or int32 [B]: batch entry b attends to its
+                              first k_lens[b] keys only (clamped to [0, Sk]), and the
+                              causal mask aligns to that end: key j is seen by row i
+                              iff j <= i + (k_lens[b] - Sq). K and V rows past it may
+                              hold anything. For caches filled to different lengths. */
+  fa_tensor o;             /* written */
+  fa_tensor o2;            /* written if o2.ptr is not NULL: O_2 = P_2 V, which the
+                              backward needs */
+  float* lse;              /* written, dense fp32 [2, B, H, Sq]: both maps' logsumexp;
+                              -inf for a row with no allowed key (its o is 0) */
+  int B, H, Hk, Sq, Sk, D, Dv;
+  float scale;
+  int causal;
+  int dtype;
+  void* workspace; /* device scratch of fa_diff_fwd_workspace_size() bytes, 256-byte
+                      aligned; may be NULL where that is 0. Used by no other call at
+                      the same time; need not be initialised. */
+  size_t workspace_bytes;
+} fa_diff_fwd_params;
+
+typedef struct {
+  fa_tensor q[2], k[2], v, o, o2, dO; /* read; o, o2 and lse are the forward's outputs */
+  const float* lse;
+  fa_diff_lambda lambda;
+  fa_tensor dq[2], dk[2], dv; /* written */
+  void* dlambda;              /* written, dense [extent_b, extent_s, extent_h], lambda's
+                                 dtype: dL/dlambda summed over the axes of extent 1 */
+  int B, H, Hk, Sq, Sk, D, Dv;
+  float scale;
+  int causal;
+  int dtype;
+  void* workspace; /* >= fa_diff_bwd_workspace_size() bytes, 256-byte aligned */
+  size_t workspace_bytes;
+  int deterministic; /* as in fa_bwd_params: 0 sums dq with fp32 atomics, 1 in
+                        key-block order; dk, dv and dlambda are always summed in a
+                        fixed order */
+} fa_diff_bwd_params;
+
+/* Forward. */
+int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream);
+
+/* Workspace bytes of fa_diff_fwd on the current device (0 for most shapes;
+   calls of few query rows over many keys split the keys over the SMs and
+   need some). Host only. 0 also for arguments that fa_diff_fwd refuses. */
+size_t fa_diff_fwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, int causal);
+
+/* Backward of L = sum(dO * O). The forward must have attended to all Sk keys
+   (k_lens NULL). */
+int fa_diff_bwd(const fa_diff_bwd_params* p, fa_stream_t stream);
+
+/* Workspace bytes of fa_diff_bwd: both maps' fp32 dq accumulators
+   [2, B, H, Sq_pad, 64] (deterministic: one [2][128][64] slot per query block
+   and key block instead), five row terms per padded row, one per row and 4 KB.
+   0 for arguments that fa_diff_bwd refuses. */
+size_t fa_diff_bwd_workspace_size(int B, int H, int Sq, int Sk, int deterministic);
+
+/* ------------------------------------------- rotary positions, several axes
+   Turns the first 2R columns of every head of q and k, as R pairs: columns
+   (j, j + R), or (2j, 2j + 1) if `interleaved`. R is the sum of `sections`:
+   the first sections[0] pairs take their position from axis 0, the next
+   sections[1] from axis 1, and so on (time, height and width of a patch, for
+   example). Pair j turns by theta_j = position * inv_freq[j]:
+       (a, b) -> (a cos - b sin, a sin + b cos);
+   `inverse` turns by -theta_j, which is also the gradient. Columns from 2R on
+   are copied. theta is reduced in fp64, so far positions keep their angle;
+   each result is rounded once. q_out may be q and k_out may be k (in place);
+   other overlaps are not allowed. Positions may be negative. */
+#define FA_ROTARY_MAX_AXES 8
+typedef struct {
+  fa_tensor q, k;         /* read: [B, S, H, D] and [B, S, Hk, D] views (alignment as above) */
+  fa_tensor q_out, k_out; /* written; k and k_out are not used when Hk is 0 */
+  const void* positions;  /* [axes, B, S], int32 or int64; any strides, 0 included */
+  int64_t pos_stride_axis, pos_stride_b, pos_stride_s;
+  int pos_int64;          /* 0: int32, 1: int64 */
+  const void* inv_freq;   /* dense [R], fp32 or fp64 */
+  int inv_freq_fp64;      /* 0: fp32, 1: fp64 */
+  int axes;               /* 1 .. FA_ROTARY_MAX_AXES */
+  int sections[FA_ROTARY_MAX_AXES]; /* pairs of each axis, >= 0; 1 <= R <= D / 2 */
+  int B, S, H, Hk, D;     /* D a multiple of 8 in [8, 256]; Hk >= 0 */
+  int interleaved, inverse;
+  int dtype;              /* FA_FP16 or FA_BF16 */
+} fa_rotary_params;
+
+int fa_rotary(const fa_rotary_params* p, fa_stream_t stream);
+
 /* Synchronises the current device, returns the status word recorded by
    kernels since the last call (FA_OK, FA_ERR_TIMEOUT or, in the check
    build, FA_ERR_BOUNDS) and clears it. FA_ERR_CUDA if the device cannot be
