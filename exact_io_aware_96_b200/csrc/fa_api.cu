@@ -121,6 +121,10 @@ int prepare(F* fn, int smem_bytes, bool (&done)[kMaxDevices]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
+  // Binds the device's primary context to this thread: a thread that has made
+  // no other CUDA call yet (an autograd worker whose buffers came from a cache)
+  // has none, and cuTensorMapEncodeTiled, a driver call, needs one.
+  if (cudaSetDevice(dev) != cudaSuccess) return FA_ERR_CUDA;
   if (!done[dev]) {
     if (smem_bytes > 0 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
