@@ -6,6 +6,7 @@
 
 #include "fa_diff_bwd.cuh"
 #include "fa_diff_fwd.cuh"
+#include "fa_diff_rows.cuh"
 #include "fa_rotary.cuh"
 
 namespace {
@@ -99,6 +100,96 @@ int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
   a.n_qblocks = (p->Sq + 127) / 128;
   const unsigned grid = unsigned(int64_t(a.n_qblocks) * p->B * p->H);
   kern<<<grid, L::kThreads, L::SMEM_ALLOC, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// The few-row form (fa_diff_rows.cuh): whether a call takes it, and its key
+// runs. A CTA streams its run at the SM's share of the memory bandwidth, two
+// CTAs to an SM; runs are cut so that the grid fills the SMs about twice over,
+// at no less than 128 keys (two tiles per warp).
+struct RowsPlan {
+  int chunk = 0, n_split = 0;  // n_split 0: the tiled kernel
+  uint64_t off_o = 0, bytes = 0;
+};
+RowsPlan rows_plan(int B, int H, int Hk, int Sq, int Sk, int Dv) {
+  RowsPlan p;
+  const int64_t R = int64_t(H / Hk) * Sq;
+  if (Sq > 16 || R > 64) return p;
+  const int sms = std::max(1, sm_count());
+  const int64_t items = int64_t(B) * Hk * ((R + 15) / 16);
+  const int64_t want = (4 * sms + items - 1) / items;  // runs per item
+  int64_t chunk = (Sk + want - 1) / want;
+  chunk = std::max<int64_t>(128, (chunk + 63) / 64 * 64);
+  p.chunk = int(std::min<int64_t>(chunk, (int64_t(Sk) + 63) / 64 * 64));
+  p.n_split = int((int64_t(Sk) + p.chunk - 1) / p.chunk);
+  if (items * p.n_split > (int64_t(1) << 31) - 1) return RowsPlan();
+  if (p.n_split > 1) {
+    const uint64_t slots = uint64_t(B) * Hk * R * p.n_split * 2;
+    p.off_o = round256(slots * sizeof(float2));
+    p.bytes = p.off_o + slots * (Dv <= 64 ? 64 : 128) * 4;
+  }
+  return p;
+}
+
+template <int DV, bool BF16>
+int launch_diff_rows(const fa_diff_fwd_params* p, const RowsPlan& plan, cudaStream_t stream) {
+  using L = fa::DiffRowsLayout<DV>;
+  static bool done[kMaxDevices] = {}, done_join[kMaxDevices] = {};
+  auto* kern = &fa::fa_diff_rows_kernel<DV, BF16>;
+  auto* join = &fa::fa_diff_rows_join<DV, BF16>;
+  int st = prepare(kern, L::SMEM_ALLOC, done);
+  if (st != FA_OK || (st = prepare(join, 0, done_join)) != FA_OK) return st;
+  CUtensorMap mk[2], mv;
+  for (int c = 0; c < 2; ++c)
+    if ((st = make_map(&mk[c], p->k[c], p->B, p->Sk, p->Hk, p->D, p->dtype, L::KT)) != FA_OK) return st;
+  if ((st = make_map(&mv, p->v, p->B, p->Sk, p->Hk, p->Dv, p->dtype, L::KT)) != FA_OK) return st;
+  fa::DiffRowsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  for (int c = 0; c < 2; ++c) {
+    a.q[c] = static_cast<const uint16_t*>(p->q[c].ptr);
+    set_strides(a.q_s[c], p->q[c]);
+  }
+  a.o = p->o.ptr;
+  a.o2 = p->o2.ptr;
+  a.lse = p->lse;
+  set_strides(a.o_s, p->o);
+  set_strides(a.o2_s, p->o2);
+  a.lam = p->lambda.ptr;
+  lam_strides(a.lam_s, p->lambda);
+  a.lam_kind = lam_kind(p->lambda);
+  a.k_lens = p->k_lens;
+  a.B = p->B, a.H = p->H, a.Hk = p->Hk, a.Sq = p->Sq, a.Sk = p->Sk;
+  a.d = p->D;
+  a.dv = p->Dv;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.causal = p->causal;
+  a.R = p->H / p->Hk * p->Sq;
+  a.n_mt = (a.R + 15) / 16;
+  a.chunk = plan.chunk;
+  a.n_split = plan.n_split;
+  if (plan.n_split > 1) {
+    if (p->workspace == nullptr || p->workspace_bytes < plan.bytes) return FA_ERR_WORKSPACE;
+    a.part_ml = static_cast<float2*>(p->workspace);
+    a.part_o = reinterpret_cast<float*>(static_cast<char*>(p->workspace) + plan.off_o);
+  }
+  const unsigned grid = unsigned(int64_t(p->B) * p->Hk * a.n_mt * a.n_split);
+  kern<<<grid, 128, L::SMEM_ALLOC, stream>>>(mk[0], mk[1], mv, a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (plan.n_split > 1) {
+    // Launched while the runs still work (programmatic dependent launch): its
+    // blocks wait on the device for the whole first grid.
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(unsigned(int64_t(p->B) * p->Hk * a.R));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, join, a) != cudaSuccess) return FA_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -257,7 +348,7 @@ extern "C" {
 
 size_t fa_diff_fwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, int causal) {
   if (check_diff(B, H, Hk, Sq, Sk, D, Dv, 1.f, causal, FA_BF16) != FA_OK) return 0;
-  return 0;
+  return size_t(rows_plan(B, H, Hk, Sq, Sk, Dv).bytes);
 }
 
 int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream) {
@@ -276,7 +367,14 @@ int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream) {
   if (p->lse == nullptr) return FA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(p->lse) & 3u) return FA_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(p->k_lens) & 3u) return FA_ERR_MISALIGNED;
+  if (p->workspace != nullptr && (reinterpret_cast<uintptr_t>(p->workspace) & 255u)) return FA_ERR_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const RowsPlan plan = rows_plan(p->B, p->H, p->Hk, p->Sq, p->Sk, p->Dv);
+  if (plan.n_split > 0) {
+    if (p->Dv <= 64)
+      return p->dtype == FA_BF16 ? launch_diff_rows<64, true>(p, plan, s) : launch_diff_rows<64, false>(p, plan, s);
+    return p->dtype == FA_BF16 ? launch_diff_rows<128, true>(p, plan, s) : launch_diff_rows<128, false>(p, plan, s);
+  }
   if (p->Dv <= 64) return p->dtype == FA_BF16 ? launch_diff_fwd<64, true>(p, s) : launch_diff_fwd<64, false>(p, s);
   return p->dtype == FA_BF16 ? launch_diff_fwd<128, true>(p, s) : launch_diff_fwd<128, false>(p, s);
 }

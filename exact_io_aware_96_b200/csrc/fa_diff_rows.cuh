@@ -1,0 +1,423 @@
+// fa_diff_rows.cuh — differential attention forward of few query rows over many
+// keys (decoding: one or a few new tokens over a key/value cache).
+//
+// The same mathematics as fa_diff_fwd.cuh. With R = (H / Hk) * Sq rows per key
+// head and R small, the call is bound by reading K_1, K_2 and V once, so the
+// kernel is built around that stream: the keys are cut into `n_split` runs,
+// one CTA per (batch, key head, run, 16 rows). All rows that share a key head
+// form one 16-row operand of m16n8k16 products, so shared heads read their
+// keys once. Each of the four warps streams its own 16-key tiles through a ring of
+// NS stages filled by TMA (its lane 0 issues the loads and the warp waits on
+// the stage's mbarrier: no producer warp, no block-wide barrier in the loop)
+// and keeps its own running maxima, sums and unnormalised O_1, O_2. The four
+// warps' results join in shared memory, the runs' in a second small kernel
+// (fa_diff_rows_join), both by the online softmax's rescaling. Two CTAs share
+// an SM, so one's start and end overlap the other's stream.
+//
+// P is split into two 16-bit terms, p = hi + lo, and multiplied with V twice:
+// the tensor cores have time to spare here, and O keeps the fp32 accuracy of P.
+#pragma once
+
+#include "fa_common.cuh"
+#include "fa_diff_fwd.cuh"
+
+namespace fa {
+
+struct DiffRowsArgs {
+  const uint16_t* q[2];
+  int64_t q_s[2][3];
+  void* o;
+  void* o2;
+  float* lse;
+  int64_t o_s[3], o2_s[3];
+  const void* lam;
+  int64_t lam_s[3];
+  int lam_kind;
+  const int* k_lens;
+  int B, H, Hk, Sq, Sk;
+  int d, dv;
+  float scale_log2;
+  int causal;
+  int R, n_mt;   // query rows of a key head, ceil(R / 16)
+  int chunk;     // keys of one run, a multiple of 64
+  int n_split;   // runs
+  float* part_o;    // [b, hk, row][n_split][2][DV]: a run's unnormalised O_c
+  float2* part_ml;  // [b, hk, row][n_split][2]: its (m, l)
+};
+
+template <int DV>
+struct DiffRowsLayout {
+  static constexpr int KT = 16;  // keys of a tile
+  static constexpr int NS = 3;   // stages of a warp's ring
+  static constexpr int VB = DV / 64;
+  static constexpr int TILE = KT * 128 * (2 + VB);  // K_1, K_2, V column blocks
+  static constexpr int RING = 4 * NS * TILE;
+  // The join's partial results [warp][map][16][DV + 4] reuse the ring.
+  static constexpr int OROW = DV + 4;
+  static constexpr int JOIN = 4 * 2 * 16 * OROW * 4;
+  static constexpr int OFF_ML = RING > JOIN ? RING : JOIN;  // [warp][map][16] (m, l)
+  static constexpr int OFF_BAR = OFF_ML + 4 * 2 * 16 * 8;
+  static constexpr int OFF_MISC = OFF_BAR + 4 * NS * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int SMEM_ALLOC = BYTES + 1024;
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// What a finished row writes: O, O_2 and both LSEs from both maps' sums.
+// x1, x2: N unnormalised columns from `col` on.
+template <int N, bool BF16, typename Args>
+__device__ __forceinline__ void diff_row_out(const Args& a, int b, int h, int row, int col, bool has, const float* x1,
+                                             const float* x2, float l1, float l2) {
+  using namespace sm100;
+  const float lam =
+      has ? load_lam(a.lam, a.lam_kind, b * a.lam_s[0] + row * a.lam_s[1] + h * a.lam_s[2]) : 0.f;
+  const float i1 = has ? 1.f / l1 : 0.f, i2 = has ? 1.f / l2 : 0.f;
+  uint32_t* po = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.o) + b * a.o_s[0] + row * a.o_s[1] +
+                                             h * a.o_s[2] + col);
+  uint32_t* po2 = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(a.o2) + b * a.o2_s[0] + row * a.o2_s[1] +
+                                              h * a.o2_s[2] + col);
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    const float y0 = has ? x2[e] * i2 : 0.f, y1 = has ? x2[e + 1] * i2 : 0.f;
+    const float z0 = has ? x1[e] * i1 : 0.f, z1 = has ? x1[e + 1] * i1 : 0.f;
+    if (col + e < a.dv) {
+      po[e / 2] = pack2<BF16>(z0 - lam * y0, z1 - lam * y1);
+      if (a.o2 != nullptr) po2[e / 2] = pack2<BF16>(y0, y1);
+    }
+  }
+}
+
+template <int DV, bool BF16>
+__global__ void __launch_bounds__(128, 2)
+    fa_diff_rows_kernel(const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmK2,
+                        const __grid_constant__ CUtensorMap tmV, const DiffRowsArgs a) {
+  using L = DiffRowsLayout<DV>;
+  using namespace sm100;
+  constexpr int KT = L::KT, NS = L::NS, NT = DV / 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  float2* ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;  // fragment row group and column pair
+
+  const int mt = static_cast<int>(blockIdx.x) % a.n_mt;
+  const int split = static_cast<int>(blockIdx.x) / a.n_mt % a.n_split;
+  const int bk = static_cast<int>(blockIdx.x) / a.n_mt / a.n_split;
+  const int hk = bk % a.Hk, b = bk / a.Hk;
+  const int group = a.H / a.Hk;
+  const int len = diff_keys(a.k_lens, b, a.Sk);
+  const int lo = split * a.chunk, hi = min(len, lo + a.chunk);
+  const int tiles = hi > lo ? (hi - lo + KT - 1) / KT : 0;
+  const int mine = tiles > warp ? (tiles - warp + 3) / 4 : 0;  // this warp's tiles: warp, warp + 4, ...
+  checked(b < a.B && mt * 16 < a.R, 601);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4 * NS; ++i) mbar_init(&bars[i], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  uint64_t* full = bars + warp * NS;
+  uint8_t* ring = smem + warp * NS * L::TILE;
+  auto issue = [&](int i) {  // lane 0: tile i of this warp into its stage
+    const int st = i % NS, key = lo + (warp + 4 * i) * KT;
+    uint8_t* dst = ring + st * L::TILE;
+    checked(key < a.Sk, 602);
+    mbar_arrive_expect_tx(&full[st], L::TILE);
+    tma_load_4d(dst, &tmK1, &full[st], 0, key, hk, b);
+    tma_load_4d(dst + KT * 128, &tmK2, &full[st], 0, key, hk, b);
+#pragma unroll
+    for (int vb = 0; vb < L::VB; ++vb) tma_load_4d(dst + (2 + vb) * KT * 128, &tmV, &full[st], vb * 64, key, hk, b);
+  };
+  if (lane == 0)
+    for (int i = 0; i < min(NS, mine); ++i) issue(i);
+
+  // Row r of the tile: query row i = r % Sq of head hk * group + r / Sq.
+  int lim[2];  // last key that rows g and g + 8 see
+  uint32_t qf[2][4][4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = mt * 16 + g + 8 * e;
+    const int i = r % a.Sq, h = hk * group + r / a.Sq;
+    lim[e] = a.causal && r < a.R ? i + len - a.Sq : len - 1;  // rows past R are not written
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint16_t* p = a.q[c] + b * a.q_s[c][0] + i * a.q_s[c][1] + h * a.q_s[c][2];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int col = ks * 16 + x * 8 + 2 * tq;
+          qf[c][ks][2 * x + e] = r < a.R && col < a.d ? *reinterpret_cast<const uint32_t*>(p + col) : 0u;
+        }
+    }
+  }
+  const int min_lim = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
+  float m[2][2], l[2][2];  // [map][row g / g + 8]
+  float acc[2][NT][4];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) m[c][e] = -INFINITY, l[c][e] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.f;
+  }
+  const float sl2 = a.scale_log2;
+  // ldmatrix row addresses: K, matrices = 16-byte chunks 0-3 of 8 keys; V,
+  // matrices = (keys 0-7, 8-15) x (chunk, chunk + 1), transposed.
+  const int kr = lane & 7, km = lane >> 3;
+  const int vr = (km & 1) * 8 + kr, vm = km >> 1;
+
+  bool ok = true;
+  int i = 0;
+  for (; i < mine; ++i) {
+    const int st = i % NS, key0 = lo + (warp + 4 * i) * KT;
+    if (!(ok = __all_sync(0xffffffffu, wait_bar(&full[st], (i / NS) & 1, abort_flag, kRoleSoftmax, i)))) break;
+    uint8_t* tile = ring + st * L::TILE;
+    const uint32_t sk = smem_u32(tile), sv = sk + 2 * KT * 128;
+    if (key0 + KT > len) {  // rows past the end count nothing, whatever they hold
+      for (int x = lane; x < L::VB * KT * 8; x += 32)
+        if (key0 + ((x >> 3) & (KT - 1)) >= len) st_shared_v4(sv + x * 16, 0, 0, 0, 0);
+      __syncwarp();
+    }
+    uint32_t ph[2][4], pl[2][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const int row = n * 8 + kr;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t f[4];
+          ldsm_x4(f, sk + c * KT * 128 + row * 128 + (((hf * 4 + km) ^ (row & 7)) << 4));
+          mma16816<BF16>(s[n], qf[c][2 * hf], f[0], f[1]);
+          mma16816<BF16>(s[n], qf[c][2 * hf + 1], f[2], f[3]);
+        }
+      }
+      const bool masked = key0 + KT - 1 > min_lim;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (masked) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (key0 + n * 8 + 2 * tq + x > lim[e]) s[n][2 * e + x] = -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx *= sl2;
+        // As in the other forwards, a stale maximum is kept within 2^8.
+        const bool raise = mx > m[c][e] + 8.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? ex2(m[c][e] - mx) : 1.f;
+          if (raise) m[c][e] = mx;
+          l[c][e] *= alpha;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[c][n][2 * e] *= alpha;
+            acc[c][n][2 * e + 1] *= alpha;
+          }
+        }
+        const float mu = m[c][e] == -INFINITY ? 0.f : m[c][e];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = ex2(fmaf(s[n][2 * e], sl2, -mu)), p1 = ex2(fmaf(s[n][2 * e + 1], sl2, -mu));
+          l[c][e] += p0 + p1;
+          const uint32_t w = pack2<BF16>(p0, p1);
+          const float2 r = unpack2<BF16>(w);
+          ph[c][2 * n + e] = w;
+          pl[c][2 * n + e] = pack2<BF16>(p0 - r.x, p1 - r.y);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t f[4];
+      ldsm_x4_t(f, sv + (n >> 3) * KT * 128 + vr * 128 + ((((n & 7) + vm) ^ (vr & 7)) << 4));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mma16816<BF16>(acc[c][n], ph[c], f[0], f[1]);
+        mma16816<BF16>(acc[c][n + 1], ph[c], f[2], f[3]);
+        mma16816<BF16>(acc[c][n], pl[c], f[0], f[1]);
+        mma16816<BF16>(acc[c][n + 1], pl[c], f[2], f[3]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && i + NS < mine) issue(i + NS);
+  }
+  if (!ok && lane == 0)  // let the copies already issued land before the CTA exits
+    for (int x = i; x < min(mine, i + NS); ++x) drain_wait(&full[x % NS], (x / NS) & 1);
+  __syncthreads();  // every warp has read its last tile: the ring becomes the join's buffer
+  if (*abort_flag) return;
+
+  float* jo = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = l[c][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (tq == 0) ml[(warp * 2 + c) * 16 + g + 8 * e] = make_float2(m[c][e], s);
+      float* row = jo + ((warp * 2 + c) * 16 + g + 8 * e) * L::OROW;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(row + n * 8 + 2 * tq) = make_float2(acc[c][n][2 * e], acc[c][n][2 * e + 1]);
+    }
+  __syncthreads();
+  // Rows of the tile x groups of 4 columns over the block's threads.
+  for (int x = threadIdx.x; x < 16 * (DV / 4); x += 128) {
+    const int tr = x / (DV / 4), col = x % (DV / 4) * 4;
+    const int r = mt * 16 + tr;
+    if (r >= a.R) break;
+    float o[2][4], mm[2], ll[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[(w * 2 + c) * 16 + tr].x);
+      mm[c] = top;
+      ll[c] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 v = ml[(w * 2 + c) * 16 + tr];
+        const float k = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2(v.x - top);  // a NaN sum stays one
+        ll[c] += v.y * k;
+        const float4 y = *reinterpret_cast<const float4*>(jo + ((w * 2 + c) * 16 + tr) * L::OROW + col);
+        o[c][0] = fmaf(y.x, k, o[c][0]);
+        o[c][1] = fmaf(y.y, k, o[c][1]);
+        o[c][2] = fmaf(y.z, k, o[c][2]);
+        o[c][3] = fmaf(y.w, k, o[c][3]);
+      }
+    }
+    const int row = r % a.Sq, h = hk * group + r / a.Sq;
+    if (a.n_split == 1) {
+      const bool has = len > 0 && (!a.causal || row + len - a.Sq >= 0);
+      diff_row_out<4, BF16>(a, b, h, row, col, has, o[0], o[1], ll[0], ll[1]);
+      if (col == 0)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          a.lse[((static_cast<int64_t>(c) * a.B + b) * a.H + h) * a.Sq + row] =
+              has ? (mm[c] + __log2f(ll[c])) * 0.69314718055994531f : -INFINITY;
+    } else {
+      const int64_t slot = (static_cast<int64_t>(bk) * a.R + r) * a.n_split + split;
+      checked(slot < static_cast<int64_t>(a.B) * a.Hk * a.R * a.n_split, 603);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        *reinterpret_cast<float4*>(a.part_o + (slot * 2 + c) * DV + col) =
+            make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+        if (col == 0) a.part_ml[slot * 2 + c] = make_float2(mm[c], ll[c]);
+      }
+    }
+  }
+}
+
+// Joins the runs of one row per block. Eight warps take every eighth run each
+// (a lane holds DV / 32 columns of both maps), then meet in shared memory.
+template <int DV, bool BF16>
+__global__ void __launch_bounds__(256) fa_diff_rows_join(const DiffRowsArgs a) {
+  using namespace sm100;
+  constexpr int N = DV / 32;
+  __shared__ float so[8][2][DV];
+  __shared__ float2 sml[8][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' results are written and visible
+  const int64_t at = blockIdx.x;  // (b, hk, r)
+  const int r = static_cast<int>(at % a.R);
+  const int bk = static_cast<int>(at / a.R);
+  const int b = bk / a.Hk;
+  const int row = r % a.Sq, h = bk % a.Hk * (a.H / a.Hk) + r / a.Sq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = diff_keys(a.k_lens, b, a.Sk);
+  const int used = (len + a.chunk - 1) / a.chunk;  // later runs have no key
+  const float2* pml = a.part_ml + at * a.n_split * 2;
+  const float* po = a.part_o + at * a.n_split * 2 * DV + lane * N;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][N];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[c][e] = 0.f;
+  // The row's maxima first, so that the runs' O are added without rescaling.
+  for (int s = lane; s < used; s += 32)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) m[c] = fmaxf(m[c], pml[s * 2 + c].x);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], x));
+#pragma unroll 4
+  for (int s = warp; s < used; s += 8)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float2 v = pml[s * 2 + c];
+      const float k = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2(v.x - m[c]);
+      l[c] += v.y * k;
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[c][e] = fmaf(po[(static_cast<int64_t>(s) * 2 + c) * DV + e], k, o[c][e]);
+    }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) so[warp][c][lane * N + e] = o[c][e];
+    if (lane == 0) sml[warp][c] = make_float2(m[c], l[c]);
+  }
+  __syncthreads();
+  if (threadIdx.x >= DV / 2) return;
+  const int col = threadIdx.x * 2;
+  float x[2][2], lt[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    x[c][0] = x[c][1] = lt[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      x[c][0] += so[w][c][col];
+      x[c][1] += so[w][c][col + 1];
+      lt[c] += sml[w][c].y;
+    }
+  }
+  const bool has = len > 0 && (!a.causal || row + len - a.Sq >= 0);
+  diff_row_out<2, BF16>(a, b, h, row, col, has, x[0], x[1], lt[0], lt[1]);
+  if (col == 0)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      a.lse[((static_cast<int64_t>(c) * a.B + b) * a.H + h) * a.Sq + row] =
+          has ? (m[c] + __log2f(lt[c])) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace fa

@@ -174,6 +174,32 @@ def test_key_lengths(fa_lib, Sq, Sk, causal):
     within("o2", o2, want["o2"], want["o2_bound"])
 
 
+ROWS = [  # B, Sq, Sk, H, Hk, D, Dv, dtype, causal: few rows over many keys
+    (1, 1, 16, 1, 1, 64, 128, torch.bfloat16, False),
+    (1, 1, 129, 8, 8, 64, 128, torch.float16, True),
+    (2, 3, 5000, 8, 2, 64, 128, torch.bfloat16, True),     # 12 rows a key head, many runs
+    (1, 16, 1111, 4, 1, 64, 64, torch.float16, True),      # 64 rows: four row tiles
+    (3, 7, 333, 6, 2, 40, 80, torch.bfloat16, False),      # 21 rows: a ragged second tile
+    (1, 16, 8, 3, 3, 16, 8, torch.float16, True),          # fewer keys than rows
+    (1, 17, 700, 4, 1, 64, 128, torch.bfloat16, True),     # one row more than the few-row form takes
+    (40, 2, 200, 4, 4, 8, 128, torch.bfloat16, True),
+]
+
+
+@pytest.mark.parametrize("c", ROWS, ids=lambda c: f"B{c[0]}q{c[1]}k{c[2]}h{c[3]}-{c[4]}d{c[5]}-{c[6]}c{int(c[8])}")
+def test_few_rows(fa_lib, c):
+    B, Sq, Sk, H, Hk, D, Dv, dtype, causal = c
+    u, t = ROUND[dtype]
+    q, k, v, lam, _ = case(B, Sq, Sk, H, Hk, D, Dv, dtype, 40 + Sk, "token")
+    want = differential(np64(q), np64(k), np64(v), np64(lam), D ** -0.5, causal, u=u, t=t)
+    o, lse, o2 = fa.diff_forward(q.cuda(), k.cuda(), v.cuda(), lam.cuda(), causal=causal, need_o2=True)
+    status_clear()
+    check_lse(lse, want["lse"])
+    within("o", o, want["o"], want["o_bound"])
+    within("o2", o2, want["o2"], want["o2_bound"])
+    close_in_norm("o", o, want["o"], 4 * u)
+
+
 def test_autograd_against_differences(fa_lib):
     """The gradients against central differences of the oracle along random directions."""
     c = case(1, 70, 90, 2, 1, 64, 128, torch.float16, 31, "head", torch.float32)
