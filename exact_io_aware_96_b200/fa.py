@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -127,6 +128,7 @@ def use_library(path: str) -> None:
     global _lib, LIB_PATH
     LIB_PATH = path
     _lib = None
+    _packed_fns.clear()
 
 
 def lib():
@@ -181,6 +183,19 @@ def lib():
         L.fa_version.restype = i
         _lib = L
     return _lib
+
+
+_packed_fns = {}
+
+
+def _packed(name: str):
+    """The entry point `name` taking its params struct as packed bytes."""
+    f = _packed_fns.get(name)
+    if f is None:
+        f = lib()[name]  # a function object of its own
+        f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
+        _packed_fns[name] = f
+    return f
 
 
 # ---------------------------------------------------------------- raw C ABI
@@ -492,14 +507,26 @@ def backward(q, k, v, o, lse, do, causal=False, scale=None, dq=None, dk=None, dv
 
 
 # ------------------------------------- differential attention, rotary positions
+# These helpers are called on single tokens, where the GPU's part is a few
+# microseconds, so they spend little on the host: parameter structs are packed
+# in one step (the layouts of DiffFwdParams, DiffBwdParams and RotaryParams;
+# "@" pads as the C compiler does), tensors are asked for their shape and
+# strides once, and the detailed checks run only where a quick one fails.
+_T = "Pqqq"  # fa_tensor
+_LAM = "Pqqqiiii"  # fa_diff_lambda
+_DIFF_FWD = struct.Struct("@" + 5 * _T + _LAM + "P" + 2 * _T + "P7ifiiPN")
+_DIFF_BWD = struct.Struct("@" + 8 * _T + "P" + _LAM + 5 * _T + "P7ifiiPNi0P")
+_ROTARY = struct.Struct("@" + 4 * _T + f"PqqqiPii{FA_ROTARY_MAX_AXES}i8i0P")
+_NO_TENSOR = (0, 0, 0, 0)
+
+
 @contextlib.contextmanager
 def _on(dev, stream):
-    """The raw handle of the launch stream on `dev`. A stream given by the
-    caller is made torch's current one meanwhile, so that what the helper
-    allocates belongs to the stream that uses it."""
+    """Makes `dev` current, and the caller's stream (if any) torch's current
+    one, so that what the helper allocates belongs to the stream that uses it."""
     with torch.cuda.device(dev):
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
+            yield
             return
         if not isinstance(stream, torch.cuda.Stream):
             raw = _stream(stream)
@@ -507,61 +534,83 @@ def _on(dev, stream):
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, q on {dev}")
         with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+            yield
 
 
-def _pair_view(t: torch.Tensor):
-    """The two maps' [B, S, H, D] views of a [B, S, H, 2, D] tensor."""
-    sb, ss, sh, sc, _ = t.stride()
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+def _current(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _flat(name: str, t: torch.Tensor):
+    """fa_tensor of a [B, S, H, D] view."""
+    sb, ss, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.data_ptr(), sb, ss, sh
+
+
+def _pair(name: str, t: torch.Tensor):
+    """The two maps' fa_tensors of a [B, S, H, 2, D] view of 16-bit values."""
+    sb, ss, sh, sc, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
     at = t.data_ptr()
-    return (FaTensor * 2)(FaTensor(at, sb, ss, sh), FaTensor(at + 2 * sc, sb, ss, sh))
+    return at, sb, ss, sh, at + 2 * sc, sb, ss, sh
+
+
+def _need(name: str, t: torch.Tensor, shape, dtype, dev) -> None:
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _expect(name, t, shape, dtype, dev)
 
 
 def _diff_dims(q, k, v):
     if q.dim() != 5 or k.dim() != 5 or v.dim() != 4 or q.shape[3] != 2 or k.shape[3] != 2:
         raise ValueError("expected q [B, Sq, H, 2, D], k [B, Sk, Hk, 2, D] and v [B, Sk, Hk, Dv]")
     B, Sq, H, _, D = q.shape
-    Sk, Hk, Dv = v.shape[1:]
-    dt = _dtype_code(q)
-    _expect("k", k, (B, Sk, Hk, 2, D), q.dtype, q.device)
-    _expect("v", v, (B, Sk, Hk, Dv), q.dtype, q.device)
+    _, Sk, Hk, Dv = v.shape
+    dt, dev = _dtype_code(q), q.device
+    _need("k", k, (B, Sk, Hk, 2, D), q.dtype, dev)
+    _need("v", v, (B, Sk, Hk, Dv), q.dtype, dev)
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} query heads cannot share {Hk} key heads evenly")
-    if not q.is_cuda:
-        raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
-    return B, Sq, H, D, Sk, Hk, Dv, dt
+    return B, Sq, H, D, Sk, Hk, Dv, dt, dev
 
 
-def _last_axis(**tensors) -> None:
-    for name, t in tensors.items():
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name}: the last axis must be contiguous")
-
-
-def _lambda(lam, B, Sq, H, q) -> DiffLambda:
+def _lambda(lam, B, Sq, H, dtype, dev):
     if not isinstance(lam, torch.Tensor) or lam.dim() > 3:
         raise ValueError("lam must be a tensor that broadcasts to [B, Sq, H]")
-    ext = (1,) * (3 - lam.dim()) + tuple(lam.shape)
-    if any(e != 1 and e != n for e, n in zip(ext, (B, Sq, H))):
+    none = 3 - lam.dim()
+    eb, es, eh = (1,) * none + tuple(lam.shape)
+    if (eb != 1 and eb != B) or (es != 1 and es != Sq) or (eh != 1 and eh != H):
         raise ValueError(f"lam: {tuple(lam.shape)} does not broadcast to [{B}, {Sq}, {H}]")
-    if lam.dtype not in (torch.float32, q.dtype):
-        raise TypeError(f"lam: expected float32 or {q.dtype}, got {lam.dtype}")
-    if lam.device != q.device:
-        raise ValueError(f"lam is on {lam.device}, q on {q.device}")
-    st = (0,) * (3 - lam.dim()) + tuple(lam.stride())
-    return DiffLambda(lam.data_ptr(), *st, *ext, FA_LAMBDA_FP32 if lam.dtype == torch.float32 else _DT[lam.dtype])
+    if lam.dtype is not torch.float32 and lam.dtype is not dtype:
+        raise TypeError(f"lam: expected float32 or {dtype}, got {lam.dtype}")
+    if lam.device != dev:
+        raise ValueError(f"lam is on {lam.device}, q on {dev}")
+    code = FA_LAMBDA_FP32 if lam.dtype is torch.float32 else _DT[lam.dtype]
+    return (lam.data_ptr(), *((0,) * none + lam.stride()), eb, es, eh, code)
 
 
 def _diff_lse(lse, B, H, Sq, dev):
-    _expect("lse", lse, (2, B, H, Sq), torch.float32, dev)
+    _need("lse", lse, (2, B, H, Sq), torch.float32, dev)
     if not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [2, B, H, Sq] tensor")
 
 
-def _ws_bytes(workspace, dev) -> int:
+def _ws(workspace, dev):
+    """(address, bytes) of a workspace, or of none."""
+    if workspace is None:
+        return 0, 0
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous buffer on {dev}")
-    return workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=False, out=None, out2=None, lse=None,
@@ -575,38 +624,37 @@ def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=Fa
     entry b attends to its first k_lens[b] keys, and the causal mask aligns to
     that end. LSE is fp32 [2, B, H, Sq]. O2 = softmax(scale q_2 k_2^T) v is
     written if need_o2 or out2 asks for it (diff_backward needs it), else None."""
-    B, Sq, H, D, Sk, Hk, Dv, dt = _diff_dims(q, k, v)
-    dev = q.device
-    lp = _lambda(lam, B, Sq, H, q)
-    if scale is None:
-        scale = D ** -0.5
+    B, Sq, H, D, Sk, Hk, Dv, dt, dev = _diff_dims(q, k, v)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return diff_forward(q, k, v, lam, causal, scale, k_lens, need_o2, out, out2, lse, workspace)
+    lp = _lambda(lam, B, Sq, H, q.dtype, dev)
     if k_lens is not None:
-        _expect("k_lens", k_lens, (B,), torch.int32, dev)
+        _need("k_lens", k_lens, (B,), torch.int32, dev)
         if not k_lens.is_contiguous():
             raise ValueError("k_lens must be contiguous")
-    with _on(dev, stream) as raw:
-        if out is None:
-            out = torch.empty((B, Sq, H, Dv), dtype=q.dtype, device=dev)
-        if out2 is None and need_o2:
-            out2 = torch.empty((B, Sq, H, Dv), dtype=q.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((2, B, H, Sq), dtype=torch.float32, device=dev)
-        _expect("out", out, (B, Sq, H, Dv), q.dtype, dev)
-        if out2 is not None:
-            _expect("out2", out2, (B, Sq, H, Dv), q.dtype, dev)
-            _last_axis(out2=out2)
+    shape, causal = (B, Sq, H, Dv), 1 if causal else 0
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    else:
+        _need("out", out, shape, q.dtype, dev)
+    if out2 is not None:
+        _need("out2", out2, shape, q.dtype, dev)
+    elif need_o2:
+        out2 = torch.empty(shape, dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((2, B, H, Sq), dtype=torch.float32, device=dev)
+    else:
         _diff_lse(lse, B, H, Sq, dev)
-        _last_axis(q=q, k=k, v=v, out=out)
-        if workspace is None:
-            n = fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, int(bool(causal)))
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        p = DiffFwdParams(_pair_view(q), _pair_view(k), _view(v), lp,
-                          k_lens.data_ptr() if k_lens is not None else None, _view(out),
-                          _view(out2) if out2 is not None else FaTensor(), lse.data_ptr(),
-                          B, H, Hk, Sq, Sk, D, Dv, float(scale), int(bool(causal)), dt,
-                          workspace.data_ptr() if workspace is not None else None,
-                          _ws_bytes(workspace, dev) if workspace is not None else 0)
-        st = fa_diff_fwd(p, raw)
+    if workspace is None:
+        n = fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    p = _DIFF_FWD.pack(*_pair("q", q), *_pair("k", k), *_flat("v", v), *lp,
+                       0 if k_lens is None else k_lens.data_ptr(), *_flat("out", out),
+                       *(_NO_TENSOR if out2 is None else _flat("out2", out2)), lse.data_ptr(),
+                       B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale), causal, dt,
+                       *_ws(workspace, dev))
+    st = _packed("fa_diff_fwd")(p, _current(dev))
     if st != FA_OK:
         raise FaError(st, "fa_diff_fwd")
     return out, lse, out2
@@ -618,32 +666,31 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=Non
     and lse it takes. dLam has lam's shape and dtype: the gradient is summed
     over the axes lam is broadcast over. ``deterministic=True`` sums dQ in a
     fixed order (dK, dV and dLam always are)."""
-    B, Sq, H, D, Sk, Hk, Dv, dt = _diff_dims(q, k, v)
-    dev = q.device
-    lp = _lambda(lam, B, Sq, H, q)
+    B, Sq, H, D, Sk, Hk, Dv, dt, dev = _diff_dims(q, k, v)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return diff_backward(q, k, v, lam, o, o2, lse, do, causal, scale, dq, dk, dv, dlam, workspace, None,
+                                 deterministic)
+    lp = _lambda(lam, B, Sq, H, q.dtype, dev)
+    shape, det = (B, Sq, H, Dv), 1 if deterministic else 0
     for name, t in (("o", o), ("o2", o2), ("do", do)):
-        _expect(name, t, (B, Sq, H, Dv), q.dtype, dev)
+        _need(name, t, shape, q.dtype, dev)
     _diff_lse(lse, B, H, Sq, dev)
-    if scale is None:
-        scale = D ** -0.5
-    with _on(dev, stream) as raw:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else dk
-        dv = torch.empty(v.shape, dtype=q.dtype, device=dev) if dv is None else dv
-        dlam = torch.empty(lam.shape, dtype=lam.dtype, device=dev) if dlam is None else dlam
-        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dlam", dlam, lam)):
-            _expect(name, t, like.shape, like.dtype, dev)
-        if not dlam.is_contiguous():
-            raise ValueError("dlam must be contiguous")
-        _last_axis(q=q, k=k, v=v, o=o, o2=o2, do=do, dq=dq, dk=dk, dv=dv)
-        if workspace is None:
-            n = fa_diff_bwd_workspace_size(B, H, Sq, Sk, int(bool(deterministic)))
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        p = DiffBwdParams(_pair_view(q), _pair_view(k), _view(v), _view(o), _view(o2), _view(do), lse.data_ptr(), lp,
-                          _pair_view(dq), _pair_view(dk), _view(dv), dlam.data_ptr(),
-                          B, H, Hk, Sq, Sk, D, Dv, float(scale), int(bool(causal)), dt,
-                          workspace.data_ptr(), _ws_bytes(workspace, dev), int(bool(deterministic)))
-        st = fa_diff_bwd(p, raw)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=q.dtype, device=dev) if dv is None else dv
+    dlam = torch.empty(lam.shape, dtype=lam.dtype, device=dev) if dlam is None else dlam
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dlam", dlam, lam)):
+        _need(name, t, like.shape, like.dtype, dev)
+    if not dlam.is_contiguous():
+        raise ValueError("dlam must be contiguous")
+    if workspace is None:
+        workspace = torch.empty(fa_diff_bwd_workspace_size(B, H, Sq, Sk, det), dtype=torch.uint8, device=dev)
+    p = _DIFF_BWD.pack(*_pair("q", q), *_pair("k", k), *_flat("v", v), *_flat("o", o), *_flat("o2", o2),
+                       *_flat("do", do), lse.data_ptr(), *lp, *_pair("dq", dq), *_pair("dk", dk), *_flat("dv", dv),
+                       dlam.data_ptr(), B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale),
+                       1 if causal else 0, dt, *_ws(workspace, dev), det)
+    st = _packed("fa_diff_bwd")(p, _current(dev))
     if st != FA_OK:
         raise FaError(st, "fa_diff_bwd")
     return dq, dk, dv, dlam
@@ -657,14 +704,18 @@ def rotary_inv_freq(sections, base=10000.0, per_axis=False, device="cuda") -> to
                         device=device)
 
 
-def _rotary_view(name: str, t: torch.Tensor) -> FaTensor:
-    """[B, S, H, D], or [B, S, H, 2, D] with the two maps as neighbouring heads."""
+def _heads(name: str, t: torch.Tensor, B, S, D, dtype, dev):
+    """(heads, fa_tensor) of [B, S, heads, D], or of [B, S, H, 2, D] with the two maps as neighbouring heads."""
     if t.dim() == 5:
         try:
             t = t.view(t.shape[0], t.shape[1], -1, t.shape[4])
         except RuntimeError:
             raise ValueError(f"{name}: the head axes of [B, S, H, 2, D] must be one run of heads") from None
-    return _view(t)
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, S, heads, D] or [B, S, H, 2, D]")
+    n = t.shape[2]
+    _need(name, t, (B, S, n, D), dtype, dev)
+    return n, _flat(name, t)
 
 
 def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
@@ -679,20 +730,16 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
     all on the only axis). Pairs are columns (j, j + R), or (2j, 2j + 1) if
     interleaved; columns from 2R on are copied. inverse turns back: it is also
     the gradient. out_q may be q and out_k may be k (in place)."""
-    dt = _dtype_code(q)
-    dev = q.device
-    if q.dim() not in (4, 5) or (k is not None and k.dim() not in (4, 5)):
-        raise ValueError("q and k must be [B, S, H, D] or [B, S, H, 2, D] tensors")
+    dt, dev, dtype = _dtype_code(q), q.device, q.dtype
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return rotary(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k)
     B, S, D = q.shape[0], q.shape[1], q.shape[-1]
-    heads = [0, 0]
-    for i, (name, t) in enumerate((("q", q), ("k", k))):
-        if t is None:
-            continue
-        _expect(name, t, (B, S, *t.shape[2:-1], D), q.dtype, dev)
-        heads[i] = t.shape[2] * (t.shape[3] if t.dim() == 5 else 1)
+    H, vq = _heads("q", q, B, S, D, dtype, dev)
+    Hk, vk = _heads("k", k, B, S, D, dtype, dev) if k is not None else (0, _NO_TENSOR)
     if positions.dim() == 2:
         positions = positions[None]
-    if positions.dim() != 3 or tuple(positions.shape[1:]) != (B, S):
+    if positions.dim() != 3 or positions.shape[1:] != (B, S):
         raise ValueError(f"positions: expected [axes, {B}, {S}], got {tuple(positions.shape)}")
     if positions.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"positions: expected int32 or int64, got {positions.dtype}")
@@ -703,33 +750,35 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
     for name, t in (("positions", positions), ("inv_freq", inv_freq)):
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, q on {dev}")
-    axes = positions.shape[0]
-    sections = (inv_freq.numel(),) if sections is None else tuple(int(n) for n in sections)
+    axes, pairs = positions.shape[0], inv_freq.shape[0]
+    sections = (pairs,) if sections is None else tuple(sections)
     if len(sections) != axes or not 1 <= axes <= FA_ROTARY_MAX_AXES:
         raise ValueError(f"sections: expected one entry for each of 1 to {FA_ROTARY_MAX_AXES} axes, got "
                          f"{len(sections)} for {axes}")
-    if sum(sections) != inv_freq.numel() or min(sections) < 0:
-        raise ValueError(f"sections {sections} do not add up to inv_freq's {inv_freq.numel()} pairs")
-    if 2 * sum(sections) > D:
-        raise ValueError(f"{sum(sections)} pairs do not fit into {D} columns")
-    with _on(dev, stream) as raw:
-        views = [_rotary_view("q", q), _rotary_view("k", k) if k is not None else FaTensor()]
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev) if out_q is None else out_q
-        _expect("out_q", out_q, q.shape, q.dtype, dev)
-        views.append(_rotary_view("out_q", out_q))
-        if k is not None:
-            out_k = torch.empty(k.shape, dtype=q.dtype, device=dev) if out_k is None else out_k
-            _expect("out_k", out_k, k.shape, q.dtype, dev)
-            views.append(_rotary_view("out_k", out_k))
-        elif out_k is not None:
+    if sum(sections) != pairs or min(sections) < 0:
+        raise ValueError(f"sections {sections} do not add up to inv_freq's {pairs} pairs")
+    if 2 * pairs > D:
+        raise ValueError(f"{pairs} pairs do not fit into {D} columns")
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=dtype, device=dev)
+    elif out_q.shape != q.shape:
+        _expect("out_q", out_q, q.shape, dtype, dev)
+    if k is None:
+        if out_k is not None:
             raise ValueError("out_k without k")
-        else:
-            views.append(FaTensor())
-        p = RotaryParams(*views, positions.data_ptr(), *positions.stride(), int(positions.dtype == torch.int64),
-                         inv_freq.data_ptr(), int(inv_freq.dtype == torch.float64), axes,
-                         (ctypes.c_int * FA_ROTARY_MAX_AXES)(*sections), B, S, heads[0], heads[1], D,
-                         int(bool(interleaved)), int(bool(inverse)), dt)
-        st = fa_rotary(p, raw)
+        wk = _NO_TENSOR
+    else:
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=dtype, device=dev)
+        elif out_k.shape != k.shape:
+            _expect("out_k", out_k, k.shape, dtype, dev)
+        wk = _heads("out_k", out_k, B, S, D, dtype, dev)[1]
+    p = _ROTARY.pack(*vq, *vk, *_heads("out_q", out_q, B, S, D, dtype, dev)[1], *wk, positions.data_ptr(),
+                     *positions.stride(), 1 if positions.dtype is torch.int64 else 0, inv_freq.data_ptr(),
+                     1 if inv_freq.dtype is torch.float64 else 0, axes,
+                     *sections, *(0,) * (FA_ROTARY_MAX_AXES - axes), B, S, H, Hk, D,
+                     1 if interleaved else 0, 1 if inverse else 0, dt)
+    st = _packed("fa_rotary")(p, _current(dev))
     if st != FA_OK:
         raise FaError(st, "fa_rotary")
     return out_q, out_k
