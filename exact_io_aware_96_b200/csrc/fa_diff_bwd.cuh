@@ -79,6 +79,32 @@ struct DiffBwdArgs {
 
 constexpr int kDiffVec = 5 * 64;  // floats of one chunk's row terms
 
+// Tensor memory in matrix-fragment order: of a warp's 32 lanes x 8 columns,
+// thread t gets rows t / 4 + {0, 8, 16, 24} and columns 2 (t % 4) + {0, 1}, where
+// the 32x32b form gives it all columns of row t. A thread then needs only a
+// quarter of the per-column constants (for four rows each).
+// 16 lanes x 32 columns (32-bit): v[4 j + 2 e + x] = row t / 4 + 8 e, column 8 j + 2 (t % 4) + x.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 lanes x 16 columns (32-bit words of two 16-bit values): r[2 j + e] = row t / 4 + 8 e, column 4 j + t % 4.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
 // ------------------------------------------------------------- preprocess
 // DV / 8 threads per (b, h, i) row, i in [0, Sq_pad).
 template <int DV, bool BF16>
@@ -456,7 +482,7 @@ __global__ void __launch_bounds__(448, 1)
       const uint32_t sDS = smem_u32(smem + L::OFF_DS);
       // S_c^T = K_c Q_c^T, dP^T = V dO^T: M = 128 keys, N = 64 queries (both K-major).
       constexpr uint32_t id_s = idesc_f16(BF16, 128, 64, 0, 0);
-      // dV += W^T dO (A in TMEM), dK_c += dS_c^T Q_c (A in smem, K-major); B MN-major, K = 64 queries.
+      // dV += W^T dO, dK_c += dS_c^T Q_c (A in TMEM); B MN-major, K = 64 queries.
       constexpr uint32_t id_v = idesc_f16(BF16, 128, DV, 0, 1);
       constexpr uint32_t id_k = idesc_f16(BF16, 128, 64, 0, 1);
       // dQ_c = dS_c K_c: M = 128 queries, N = 64, K = 128 keys; A = dS_c^T viewed MN-major, B = K_c MN-major.
@@ -494,15 +520,18 @@ __global__ void __launch_bounds__(448, 1)
         }
         mma_ts_x4(tmem + L::COL_DV, pa, bd, id_v, acc);
       };
-      auto issue_dK = [&](int st, int hf, uint32_t acc) {
+      auto issue_dK = [&](int st, uint32_t acc) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint64_t a0 = desc_sw128(sDS + (c * 2 + hf) * L::BLK, 16, 1024);
           const uint64_t b0 = desc_sw128(sQ + (st * 2 + c) * L::HBLK, L::HBLK, 1024);
-          uint64_t ad[4], bd[4];
+          uint32_t pa[4];
+          uint64_t bd[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) ad[u] = desc_add(a0, u * 32), bd[u] = desc_add(b0, u * 2048);
-          mma_ss_x4(tmem + L::COL_DK + 64 * c, ad, bd, id_k, acc);
+          for (int u = 0; u < 4; ++u) {
+            pa[u] = tmem + L::COL_DP + (u >> 1) * 32 + 16 * c + (u & 1) * 8;  // dS_c^T of queries 16u .. 16u + 15
+            bd[u] = desc_add(b0, u * 2048);
+          }
+          mma_ts_x4(tmem + L::COL_DK + 64 * c, pa, bd, id_k, acc);
         }
       };
       auto issue_dQ = [&](int c) {
@@ -557,7 +586,7 @@ __global__ void __launch_bounds__(448, 1)
           issue_dQ(0);
           mma_commit_w(dq_full);
         }
-        issue_dK(st, i & 1, i > 0);
+        issue_dK(st, i > 0);
         mma_commit_w(&q_empty[st]);
         if (i + 1 < n) {
           if (!(ok = wait(&o_full[sn], phn, i + 1))) break;
@@ -578,13 +607,16 @@ __global__ void __launch_bounds__(448, 1)
       drain_wait(drain, 0);
     }
   } else if (warp < 8) {
-    // ------------------- P and dS: one key row per thread, 32 query columns per warpgroup
+    // ------------------- P and dS: 32 keys per warp, 32 query columns per warpgroup, in fragment order
     const int g = warp >> 2;
-    const int kr = (warp & 3) * 32 + lane;
+    const int wq = warp & 3;
+    const int kr = wq * 32 + lane;  // this lane's row where a lane owns one (stores, epilogue)
     const int key = n0 + kr;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int fr = lane >> 2, fc = 2 * (lane & 3);  // fragment row and column pair
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS1 = tmem + lane_base + L::COL_S + 32 * g;
     const uint32_t tDP = tmem + lane_base + L::COL_DP + 32 * g;
+    constexpr uint32_t kUpper = 16u << 16;  // the warp's lanes 16-31
     const float sl2 = a.scale_log2;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
@@ -593,107 +625,114 @@ __global__ void __launch_bounds__(448, 1)
                                        wait_bar(&q_full[st], (i / ST) & 1, abort_flag, kRoleSoftmax, i));
       if (!ok) break;
       tc_fence_after();
-      // Query columns e < cm of this warpgroup's 32 are masked for this key
-      // (causal); all of them if key >= Sk.
-      int cm = a.causal ? key - off - chunk_row(i) - 32 * g : -1;
-      if (key >= a.Sk) cm = 32;
-      const float* vec = s_vec + st * kDiffVec + 32 * g;
+      // Query column e of this warpgroup's 32 is masked for key k if e < k + cm0
+      // (causal), or if k is past the end.
+      const int cm0 = a.causal ? n0 + wq * 32 - off - chunk_row(i) - 32 * g : -256;
+      const bool masked = cm0 + 31 > 0 || n0 + wq * 32 + 31 >= a.Sk;
+      const float* vec = s_vec + st * kDiffVec + 32 * g + fc;
       // Phase A: p1 = P_1^T, p2 = -lambda P_2^T (fp32, kept), W^T = p1 + p2 in
       // 16 bits over S_1^T.
-      uint32_t p1[32], p2[32];
-      tmem_ld32(tS1, p1);
-      tmem_ld32(tS1 + 64, p2);
+      uint32_t p1[2][16], p2[2][16];
+      tmem_ld_frag(tS1, p1[0]);
+      tmem_ld_frag(tS1 + kUpper, p1[1]);
+      tmem_ld_frag(tS1 + 64, p2[0]);
+      tmem_ld_frag(tS1 + 64 + kUpper, p2[1]);
       tmem_ld_wait();
-      reg_fence(p1);
-      reg_fence(p2);
+      reg_fence(p1[0]);
+      reg_fence(p1[1]);
+      reg_fence(p2[0]);
+      reg_fence(p2[1]);
       {
-        uint32_t w[16];
-        auto block = [&](auto masked) {
+        uint32_t w[2][8];
+        auto block = [&](auto masked_t) {
           const uint64_t sl2x2 = f2(sl2, sl2);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float4 la = reinterpret_cast<const float4*>(vec)[u];
-            const float4 lb = reinterpret_cast<const float4*>(vec + 64)[u];
-            const float4 nl = reinterpret_cast<const float4*>(vec + 128)[u];
+          for (int j = 0; j < 4; ++j) {
+            const float2 la = *reinterpret_cast<const float2*>(vec + 8 * j);
+            const float2 lb = *reinterpret_cast<const float2*>(vec + 64 + 8 * j);
+            const float2 nl = *reinterpret_cast<const float2*>(vec + 128 + 8 * j);
+            const uint64_t nla = f2(-la.x, -la.y), nlb = f2(-lb.x, -lb.y);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int e = 4 * u + 2 * hf;
-              float x0 = __uint_as_float(p1[e]), x1 = __uint_as_float(p1[e + 1]);
-              float y0 = __uint_as_float(p2[e]), y1 = __uint_as_float(p2[e + 1]);
-              const float la0 = hf ? la.z : la.x, la1 = hf ? la.w : la.y;
-              const float lb0 = hf ? lb.z : lb.x, lb1 = hf ? lb.w : lb.y;
-              const float nl0 = hf ? nl.z : nl.x, nl1 = hf ? nl.w : nl.y;
-              if constexpr (decltype(masked)::value) {
+            for (int re = 0; re < 4; ++re) {  // rows fr + 8 re
+              const int hh = re >> 1, e = re & 1, at = 4 * j + 2 * e;
+              float x0 = __uint_as_float(p1[hh][at]), x1 = __uint_as_float(p1[hh][at + 1]);
+              float y0 = __uint_as_float(p2[hh][at]), y1 = __uint_as_float(p2[hh][at + 1]);
+              if constexpr (decltype(masked_t)::value) {
                 // Masked entries are exactly 0 (MUFU of -inf).
-                x0 = (e < cm) ? -INFINITY : x0;
-                x1 = (e + 1 < cm) ? -INFINITY : x1;
-                y0 = (e < cm) ? -INFINITY : y0;
-                y1 = (e + 1 < cm) ? -INFINITY : y1;
-                x0 = ex2(fmaf(x0, sl2, -la0));
-                x1 = ex2(fmaf(x1, sl2, -la1));
-                y0 = ex2(fmaf(y0, sl2, -lb0));
-                y1 = ex2(fmaf(y1, sl2, -lb1));
-              } else {
-                const uint64_t tx = fma2(f2(x0, x1), sl2x2, f2(-la0, -la1));
-                const uint64_t ty = fma2(f2(y0, y1), sl2x2, f2(-lb0, -lb1));
-                f2_split(tx, x0, x1);
-                x0 = ex2(x0);
-                x1 = ex2(x1);
-                if (hf) {  // one pair in four on the FMA pipe
-                  f2_split(exp2_poly2(ty), y0, y1);
-                } else {
-                  f2_split(ty, y0, y1);
-                  y0 = ex2(y0);
-                  y1 = ex2(y1);
-                }
+                const int k = fr + 8 * re;
+                const int cm = n0 + wq * 32 + k >= a.Sk ? 32 : k + cm0;
+                const bool h0 = 8 * j + fc < cm, h1 = 8 * j + fc + 1 < cm;
+                x0 = h0 ? -INFINITY : x0;
+                x1 = h1 ? -INFINITY : x1;
+                y0 = h0 ? -INFINITY : y0;
+                y1 = h1 ? -INFINITY : y1;
               }
-              y0 *= nl0;
-              y1 *= nl1;
-              p1[e] = __float_as_uint(x0), p1[e + 1] = __float_as_uint(x1);
-              p2[e] = __float_as_uint(y0), p2[e + 1] = __float_as_uint(y1);
-              w[e >> 1] = pack2<BF16>(x0 + y0, x1 + y1);
+              const uint64_t tx = fma2(f2(x0, x1), sl2x2, nla);
+              const uint64_t ty = fma2(f2(y0, y1), sl2x2, nlb);
+              f2_split(tx, x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              if (!decltype(masked_t)::value && (re & 1)) {  // one pair in four on the FMA pipe
+                f2_split(exp2_poly2(ty), y0, y1);
+              } else {
+                f2_split(ty, y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+              }
+              y0 *= nl.x;
+              y1 *= nl.y;
+              p1[hh][at] = __float_as_uint(x0), p1[hh][at + 1] = __float_as_uint(x1);
+              p2[hh][at] = __float_as_uint(y0), p2[hh][at + 1] = __float_as_uint(y1);
+              w[hh][2 * j + e] = pack2<BF16>(x0 + y0, x1 + y1);
             }
           }
         };
-        if (__any_sync(0xffffffffu, cm > 0))
+        if (masked)
           block(std::true_type{});
         else
           block(std::false_type{});
-        tmem_st16(tS1, w);  // this warpgroup's own 32 columns of S_1, read above
+        tmem_st_frag(tS1, w[0]);  // this warpgroup's own columns of S_1, read above
+        tmem_st_frag(tS1 + kUpper, w[1]);
       }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(w_ready);
-      // Phase B: dS_1 = p1 (dP - Delta_1), dS_2 = p2 (dP - Delta_2), 16 bits,
-      // into swizzled shared memory.
+      // Phase B: dS_1 = p1 (dP - Delta_1), dS_2 = p2 (dP - Delta_2) in 16 bits,
+      // into tensor memory over dP (the A operands of dK: 16 columns each) and
+      // into swizzled shared memory (the A operands of dQ).
       ok = __all_sync(0xffffffffu, wait_bar(dp_full, i & 1, abort_flag, kRoleSoftmax, i) &&
                                        wait_bar(ds_free, ((i >> 1) & 1) ^ 1, abort_flag, kRoleSoftmax, i));
       if (!ok) break;
       tc_fence_after();
-      uint32_t dp[32];
-      tmem_ld32(tDP, dp);
+      uint32_t dp[2][16];
+      tmem_ld_frag(tDP, dp[0]);
+      tmem_ld_frag(tDP + kUpper, dp[1]);
       tmem_ld_wait();
-      reg_fence(dp);
+      reg_fence(dp[0]);
+      reg_fence(dp[1]);
       const uint32_t row1 = smem_u32(smem + L::OFF_DS + (i & 1) * L::BLK) + kr * 128;
-      const uint32_t row2 = row1 + 2 * L::BLK;
+      uint32_t d1[2][8], d2[2][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {  // 8 queries: one 16-byte chunk of each map's row
-        uint32_t d1[4], d2[4];
+      for (int j = 0; j < 4; ++j) {
+        const float2 da = *reinterpret_cast<const float2*>(vec + 192 + 8 * j);
+        const float2 db = *reinterpret_cast<const float2*>(vec + 256 + 8 * j);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const float4 da = reinterpret_cast<const float4*>(vec + 192)[2 * u + v];
-          const float4 db = reinterpret_cast<const float4*>(vec + 256)[2 * u + v];
-          const int e = 8 * u + 4 * v;
+        for (int re = 0; re < 4; ++re) {
+          const int hh = re >> 1, e = re & 1, at = 4 * j + 2 * e;
           auto f = [](uint32_t x) { return __uint_as_float(x); };
-          d1[2 * v] = pack2<BF16>(f(p1[e]) * (f(dp[e]) - da.x), f(p1[e + 1]) * (f(dp[e + 1]) - da.y));
-          d1[2 * v + 1] = pack2<BF16>(f(p1[e + 2]) * (f(dp[e + 2]) - da.z), f(p1[e + 3]) * (f(dp[e + 3]) - da.w));
-          d2[2 * v] = pack2<BF16>(f(p2[e]) * (f(dp[e]) - db.x), f(p2[e + 1]) * (f(dp[e + 1]) - db.y));
-          d2[2 * v + 1] = pack2<BF16>(f(p2[e + 2]) * (f(dp[e + 2]) - db.z), f(p2[e + 3]) * (f(dp[e + 3]) - db.w));
+          const float g0 = f(dp[hh][at]), g1 = f(dp[hh][at + 1]);
+          d1[hh][2 * j + e] = pack2<BF16>(f(p1[hh][at]) * (g0 - da.x), f(p1[hh][at + 1]) * (g1 - da.y));
+          d2[hh][2 * j + e] = pack2<BF16>(f(p2[hh][at]) * (g0 - db.x), f(p2[hh][at + 1]) * (g1 - db.y));
         }
-        const uint32_t at = ((4 * g + u) ^ (kr & 7)) << 4;
-        st_shared_v4(row1 + at, d1[0], d1[1], d1[2], d1[3]);
-        st_shared_v4(row2 + at, d2[0], d2[1], d2[2], d2[3]);
+        const uint32_t sw = ((4 * g + j) ^ (kr & 7)) << 4;
+        stsm_x4(row1 + sw, d1[0][2 * j], d1[0][2 * j + 1], d1[1][2 * j], d1[1][2 * j + 1]);
+        stsm_x4(row1 + 2 * L::BLK + sw, d2[0][2 * j], d2[0][2 * j + 1], d2[1][2 * j], d2[1][2 * j + 1]);
       }
+      tmem_st_frag(tDP, d1[0]);
+      tmem_st_frag(tDP + kUpper, d1[1]);
+      tmem_st_frag(tDP + 16, d2[0]);
+      tmem_st_frag(tDP + 16 + kUpper, d2[1]);
+      tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(ds_ready);
