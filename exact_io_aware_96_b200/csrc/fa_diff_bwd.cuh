@@ -42,9 +42,9 @@
 //   warp  12    TMA loader: K_1, K_2, V once; Q_1, Q_2 with the row terms, and
 //               dO, per chunk
 //   warp  13    MMA issuer
-// MMA order per chunk i: dV(i), S_1(i+1), S_2(i+1), [dQ_1], dK_1(i), dK_2(i),
-// dP(i+1), [dQ_2], with dQ after odd chunks: the softmax of chunk i+1 starts
-// while dK(i), dP(i+1) and dQ run.
+// MMA order per chunk i: dV(i), S_1(i+1), S_2(i+1), [dQ], dK_1(i), dK_2(i),
+// dP(i+1), with dQ_1 in odd chunks and dQ_2 in the even ones after them: the
+// softmax of chunk i+1 starts while dK(i), dP(i+1) and dQ run.
 #pragma once
 
 #include <type_traits>
@@ -67,7 +67,7 @@ struct DiffBwdArgs {
   void* dv;
   int64_t o_s[3], o2_s[3], do_s[3], dq_s[2][3], dk_s[2][3], dv_s[3];
   float* dq_acc;   // fp32 [2][B*H][Sq_pad][64]
-  float* vec;      // fp32 [B*H][Sq_pad / 64][5][64]: lse2_1, lse2_2, -lambda, Delta_1, Delta_2
+  float* vec;      // fp32 [B*H][Sq_pad / 64][5][64]: -lse2_1, -lse2_2, -lambda, -Delta_1, -Delta_2
   float* drow;     // fp32 [B][H][Sq]: -Delta_2
   float* dq_part;  // deterministic mode: fp32 [B*H][nqb][nkb][2][128][64] slots; else null
   int B, H, Hk, Sq, Sk, Sq_pad;
@@ -98,6 +98,21 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The 64-bit descriptor of a 128-byte-swizzled operand from its low word
+// (address >> 4 and lbo >> 4 << 16); the high word is the same for all: 1024
+// bytes between 8-row groups, the sm_100 version and the swizzle mode.
+__device__ __forceinline__ uint64_t desc_words(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"((1024u >> 4) | (1u << 14) | (2u << 29)));
+  return d;
+}
+
 // Four 8 x 8 matrices of 16-bit values; lane l gives the address of row l % 8 of matrix l / 8.
 __device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
@@ -169,11 +184,11 @@ __global__ void __launch_bounds__(256) fa_diff_pre(const DiffBwdArgs a) {
       a.drow[at] = -d_2;
     }
     float* v = a.vec + (static_cast<int64_t>(bh) * (a.Sq_pad / 64) + i / 64) * kDiffVec + (i & 63);
-    v[0] = l1;
-    v[64] = l2;
+    v[0] = -l1;
+    v[64] = -l2;
     v[128] = -lam;
-    v[192] = lam == 0.f ? d_o : fmaf(lam, d_2, d_o);
-    v[256] = d_2;
+    v[192] = -(lam == 0.f ? d_o : fmaf(lam, d_2, d_o));
+    v[256] = -d_2;
   }
 }
 
@@ -315,16 +330,22 @@ struct DiffBwdLayout {
   static constexpr int OFF_V = OFF_K + 2 * BLK;
   static constexpr int OFF_Q = OFF_V + VB * BLK;        // [stage][map][64 rows]
   static constexpr int OFF_DO = OFF_Q + ST * 2 * HBLK;  // [stage][column block][64 rows]
-  static constexpr int OFF_DS = OFF_DO + ST * VB * HBLK;  // dS_c^T: [map][chunk half][128 keys][64 queries]
-  static constexpr int OFF_DQS = OFF_DS + 4 * BLK;      // dQ staging: 4 KB per drain warp
+  static constexpr int OFF_DS = OFF_DO + ST * VB * HBLK;  // dS_1^T: [chunk half][128 keys][64 queries]
+  // dS_2^T's first half alternates between blocks 0 and 2, so that dQ_2 of a
+  // block may still read its dS while the next block's is written.
+  static constexpr int OFF_DS2 = OFF_DS + 2 * BLK;
+  static constexpr int OFF_DQS = OFF_DS2 + 3 * BLK;     // dQ staging: 4 KB per drain warp
   static constexpr int OFF_VEC = OFF_DQS + 4 * 4096;
   static constexpr int OFF_BAR = OFF_VEC + ST * kDiffVec * 4;
-  // kv_full, q_full/q_empty[ST], o_full/o_empty[ST], s_full, w_ready, dp_full, ds_ready, ds_free, dq_full,
-  // dq_free, mma_done, drain
-  static constexpr int NBAR = 1 + 4 * ST + 9;
+  // kv_full, q_full/q_empty[ST], o_full/o_empty[ST], s_full, w_ready, dp_full, ds_ready, dq_full, dq_free,
+  // mma_done, drain
+  static constexpr int NBAR = 1 + 4 * ST + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
-  static constexpr int SMEM_ALLOC = BYTES + 1024;
+  static constexpr int SMEM_MAX = 232448;
+  // Room to align the base to 1024 bytes where there is some; else the kernel
+  // requires (and checks) an aligned base.
+  static constexpr int SMEM_ALLOC = BYTES + 1024 <= SMEM_MAX ? BYTES + 1024 : BYTES;
   static constexpr int TMEM_COLS = 512;
   static constexpr int COL_DV = 0;
   static constexpr int COL_DK = 128;  // dK_1, dK_2: 64 columns each
@@ -342,10 +363,16 @@ __global__ void __launch_bounds__(448, 1)
   using L = DiffBwdLayout<DV>;
   using namespace sm100;
   constexpr int ST = L::ST;
-  static_assert(L::SMEM_ALLOC <= 232448, "smem budget");
+  static_assert(ST == 2, "the MMA warp unrolls its loop by the stages");
+  static_assert(L::BYTES <= L::SMEM_MAX, "smem budget");
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t pad = (1024 - (smem_u32(smem_raw) & 1023)) & 1023;
+  uint8_t* smem = smem_raw + pad;
+  if (L::BYTES + pad > L::SMEM_ALLOC) {
+    if (threadIdx.x == 0) atomicCAS(&g_status[0], 0, -2);
+    return;
+  }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -357,8 +384,7 @@ __global__ void __launch_bounds__(448, 1)
   uint64_t* w_ready = s_full + 1;
   uint64_t* dp_full = w_ready + 1;
   uint64_t* ds_ready = dp_full + 1;
-  uint64_t* ds_free = ds_ready + 1;
-  uint64_t* dq_full = ds_free + 1;
+  uint64_t* dq_full = ds_ready + 1;
   uint64_t* dq_free = dq_full + 1;
   uint64_t* mma_done = dq_free + 1;
   uint64_t* drain = mma_done + 1;
@@ -395,12 +421,11 @@ __global__ void __launch_bounds__(448, 1)
       mbar_init(&o_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(w_ready, 256);
+    mbar_init(w_ready, 8);  // one arrival per softmax warp
     mbar_init(dp_full, 1);
-    mbar_init(ds_ready, 256);
-    mbar_init(ds_free, 1);
+    mbar_init(ds_ready, 8);
     mbar_init(dq_full, 1);
-    mbar_init(dq_free, 128);
+    mbar_init(dq_free, 4);
     mbar_init(mma_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -473,13 +498,8 @@ __global__ void __launch_bounds__(448, 1)
     // ------------------------------------------------------------- MMA issuer
     if (n > 0) {
       auto wait = [&](uint64_t* bar, uint32_t parity, int iter) {
-        return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, kRoleMma, iter));
+        return __all_sync(0xffffffffu, wait_bar_c(bar, parity, abort_flag, kRoleMma, iter));
       };
-      const uint32_t sK = smem_u32(smem + L::OFF_K);
-      const uint32_t sV = smem_u32(smem + L::OFF_V);
-      const uint32_t sQ = smem_u32(smem + L::OFF_Q);
-      const uint32_t sdO = smem_u32(smem + L::OFF_DO);
-      const uint32_t sDS = smem_u32(smem + L::OFF_DS);
       // S_c^T = K_c Q_c^T, dP^T = V dO^T: M = 128 keys, N = 64 queries (both K-major).
       constexpr uint32_t id_s = idesc_f16(BF16, 128, 64, 0, 0);
       // dV += W^T dO, dK_c += dS_c^T Q_c (A in TMEM); B MN-major, K = 64 queries.
@@ -487,66 +507,75 @@ __global__ void __launch_bounds__(448, 1)
       constexpr uint32_t id_k = idesc_f16(BF16, 128, 64, 0, 1);
       // dQ_c = dS_c K_c: M = 128 queries, N = 64, K = 128 keys; A = dS_c^T viewed MN-major, B = K_c MN-major.
       constexpr uint32_t id_q = idesc_f16(BF16, 128, 64, 1, 1);
+      // Operand descriptors differ in their low words only (address and lbo), by
+      // constants once the stage is one: the chunk loop is unrolled by the two
+      // stages, and every operand is one addition away. The issuing warp's own
+      // instructions, not the tensor core, were what a chunk waited for before
+      // (490 -> 4xx us at S = 8192).
+      const uint32_t base = smem_u32(smem) >> 4;
+      auto desc = [&](uint32_t off, uint32_t lbo) { return desc_words(base + (off >> 4) + ((lbo >> 4) << 16)); };
       auto issue_S = [&](int st) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint64_t a0 = desc_sw128(sK + c * L::BLK, 16, 1024);
-          const uint64_t b0 = desc_sw128(sQ + (st * 2 + c) * L::HBLK, 16, 1024);
           uint64_t ad[4], bd[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) ad[u] = desc_add(a0, u * 32), bd[u] = desc_add(b0, u * 32);
+          for (int u = 0; u < 4; ++u) {
+            ad[u] = desc(L::OFF_K + c * L::BLK + u * 32, 16);
+            bd[u] = desc(L::OFF_Q + (st * 2 + c) * L::HBLK + u * 32, 16);
+          }
           mma_ss_x4(tmem + L::COL_S + 64 * c, ad, bd, id_s, 0);
         }
       };
       auto issue_dP = [&](int st) {
 #pragma unroll
         for (int vb = 0; vb < L::VB; ++vb) {
-          const uint64_t a0 = desc_sw128(sV + vb * L::BLK, 16, 1024);
-          const uint64_t b0 = desc_sw128(sdO + (st * L::VB + vb) * L::HBLK, 16, 1024);
           uint64_t ad[4], bd[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) ad[u] = desc_add(a0, u * 32), bd[u] = desc_add(b0, u * 32);
+          for (int u = 0; u < 4; ++u) {
+            ad[u] = desc(L::OFF_V + vb * L::BLK + u * 32, 16);
+            bd[u] = desc(L::OFF_DO + (st * L::VB + vb) * L::HBLK + u * 32, 16);
+          }
           mma_ss_x4(tmem + L::COL_DP, ad, bd, id_s, vb > 0);
         }
       };
       auto issue_dV = [&](int st, uint32_t acc) {
-        const uint64_t b0 = desc_sw128(sdO + st * L::VB * L::HBLK, L::HBLK, 1024);
         uint32_t pa[4];
         uint64_t bd[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           pa[u] = tmem + L::COL_S + (u >> 1) * 32 + (u & 1) * 8;  // W^T of queries 16u .. 16u + 15
-          bd[u] = desc_add(b0, u * 2048);
+          bd[u] = desc(L::OFF_DO + st * L::VB * L::HBLK + u * 2048, L::HBLK);
         }
         mma_ts_x4(tmem + L::COL_DV, pa, bd, id_v, acc);
       };
       auto issue_dK = [&](int st, uint32_t acc) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint64_t b0 = desc_sw128(sQ + (st * 2 + c) * L::HBLK, L::HBLK, 1024);
           uint32_t pa[4];
           uint64_t bd[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             pa[u] = tmem + L::COL_DP + (u >> 1) * 32 + 16 * c + (u & 1) * 8;  // dS_c^T of queries 16u .. 16u + 15
-            bd[u] = desc_add(b0, u * 2048);
+            bd[u] = desc(L::OFF_Q + (st * 2 + c) * L::HBLK + u * 2048, L::HBLK);
           }
           mma_ts_x4(tmem + L::COL_DK + 64 * c, pa, bd, id_k, acc);
         }
       };
-      auto issue_dQ = [&](int c) {
-        const uint64_t a0 = desc_sw128(sDS + c * 2 * L::BLK, L::BLK, 1024);
-        const uint64_t b0 = desc_sw128(sK + c * L::BLK, L::BLK, 1024);
+      // dQ_1; dQ_2 of a block with dS_2's first half in block 0, or (alt) in
+      // block 2: then the second half comes first, and the rows change places.
+      auto issue_dQ = [&](int c, uint32_t alt) {
+        const uint32_t a0 = (c == 0 ? L::OFF_DS : L::OFF_DS2) + alt * L::BLK;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint64_t ad[4], bd[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            ad[u] = desc_add(a0, (4 * hf + u) * 2048);
-            bd[u] = desc_add(b0, (4 * hf + u) * 2048);
+            ad[u] = desc(a0 + (4 * hf + u) * 2048, L::BLK);
+            bd[u] = desc(L::OFF_K + c * L::BLK + (4 * hf + u) * 2048, L::BLK);
           }
           mma_ss_x4(tmem + L::COL_DQ, ad, bd, id_q, hf > 0);
         }
+        mma_commit_w(dq_full);
       };
       bool ok = wait(kv_full, 0, -1) && wait(&q_full[0], 0, 0);
       if (ok) {
@@ -560,47 +589,53 @@ __global__ void __launch_bounds__(448, 1)
         issue_dP(0);
         mma_commit_w(dp_full);
       }
-      for (int i = 0; ok && i < n; ++i) {
-        const int st = i % ST, sn = (i + 1) % ST;
-        const uint32_t phn = ((i + 1) / ST) & 1;
-        const bool odd = i & 1;
-        const int blk = i >> 1;
-        if (!(ok = wait(w_ready, i & 1, i))) break;
+      // Chunk i = 2 blk + st (the number of chunks is even and ST is 2, so a
+      // chunk's stage is its half of the block, and q_full, o_full have
+      // completed blk times before).
+      auto chunk = [&](int blk, auto half) -> bool {
+        constexpr int st = decltype(half)::value, sn = st ^ 1;
+        const int i = 2 * blk + st;
+        const uint32_t phn = (blk + st) & 1;  // phase of chunk i + 1's loads
+        const bool more = i + 1 < n;
+        if (!wait(w_ready, st, i)) return false;
         tc_fence_after();
         issue_dV(st, i > 0);
-        if (i + 1 < n) {
+        mma_commit_w(&o_empty[st]);  // dP(i), issued before, and dV(i) are dO(i)'s readers
+        if (more) {
           // S(i+1) goes over S(i) and W(i): the softmax warps have read S(i)
           // (w_ready) and dV(i), issued before, reads W(i) first.
-          if (!(ok = wait(&q_full[sn], phn, i + 1))) break;
-          tc_fence_after();
+          if (!wait(&q_full[sn], phn, i + 1)) return false;
           issue_S(sn);
           mma_commit_w(s_full);
         }
-        if (!(ok = wait(ds_ready, i & 1, i))) break;
-        tc_fence_after();
-        mma_commit_w(&o_empty[st]);  // dV(i) and dP(i), issued before, were dO(i)'s last readers
-        if (odd) {
-          // The dQ buffer's use 2 blk + c waits for the drain of the use before.
-          if (blk > 0 && !(ok = wait(dq_free, (2 * blk - 1) & 1, i))) break;
+        if (st == 0 && blk > 0) {
+          // dQ_2 of the block before, once dQ_1 has been drained.
+          if (!wait(dq_free, 0, i)) return false;
           tc_fence_after();
-          issue_dQ(0);
-          mma_commit_w(dq_full);
+          issue_dQ(1, (blk - 1) & 1);
+        }
+        if (!wait(ds_ready, st, i)) return false;
+        tc_fence_after();
+        if (st) {
+          if (blk > 0 && !wait(dq_free, 1, i)) return false;  // the block before's dQ_2 has been drained
+          tc_fence_after();
+          issue_dQ(0, 0);
         }
         issue_dK(st, i > 0);
         mma_commit_w(&q_empty[st]);
-        if (i + 1 < n) {
-          if (!(ok = wait(&o_full[sn], phn, i + 1))) break;
-          tc_fence_after();
+        if (more) {
+          if (!wait(&o_full[sn], phn, i + 1)) return false;
           issue_dP(sn);
           mma_commit_w(dp_full);
         }
-        if (odd) {
-          if (!(ok = wait(dq_free, (2 * blk) & 1, i))) break;
-          tc_fence_after();
-          issue_dQ(1);
-          mma_commit_w(dq_full);
-          mma_commit_w(ds_free);
-        }
+        return true;
+      };
+      const int blocks = n / 2;
+      for (int blk = 0; ok && blk < blocks; ++blk)
+        ok = chunk(blk, std::integral_constant<int, 0>{}) && chunk(blk, std::integral_constant<int, 1>{});
+      if (ok && (ok = wait(dq_free, 0, n))) {
+        tc_fence_after();
+        issue_dQ(1, (blocks - 1) & 1);
       }
       mma_commit_w(mma_done);
       mma_commit_w(drain);
@@ -621,8 +656,8 @@ __global__ void __launch_bounds__(448, 1)
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int st = i % ST;
-      ok = __all_sync(0xffffffffu, wait_bar(s_full, i & 1, abort_flag, kRoleSoftmax, i) &&
-                                       wait_bar(&q_full[st], (i / ST) & 1, abort_flag, kRoleSoftmax, i));
+      ok = __all_sync(0xffffffffu, wait_bar_c(s_full, i & 1, abort_flag, kRoleSoftmax, i) &&
+                                       wait_bar_c(&q_full[st], (i / ST) & 1, abort_flag, kRoleSoftmax, i));
       if (!ok) break;
       tc_fence_after();
       // Query column e of this warpgroup's 32 is masked for key k if e < k + cm0
@@ -648,10 +683,9 @@ __global__ void __launch_bounds__(448, 1)
           const uint64_t sl2x2 = f2(sl2, sl2);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 la = *reinterpret_cast<const float2*>(vec + 8 * j);
-            const float2 lb = *reinterpret_cast<const float2*>(vec + 64 + 8 * j);
-            const float2 nl = *reinterpret_cast<const float2*>(vec + 128 + 8 * j);
-            const uint64_t nla = f2(-la.x, -la.y), nlb = f2(-lb.x, -lb.y);
+            const uint64_t nla = *reinterpret_cast<const uint64_t*>(vec + 8 * j);
+            const uint64_t nlb = *reinterpret_cast<const uint64_t*>(vec + 64 + 8 * j);
+            const uint64_t nl = *reinterpret_cast<const uint64_t*>(vec + 128 + 8 * j);
 #pragma unroll
             for (int re = 0; re < 4; ++re) {  // rows fr + 8 re
               const int hh = re >> 1, e = re & 1, at = 4 * j + 2 * e;
@@ -669,21 +703,23 @@ __global__ void __launch_bounds__(448, 1)
               }
               const uint64_t tx = fma2(f2(x0, x1), sl2x2, nla);
               const uint64_t ty = fma2(f2(y0, y1), sl2x2, nlb);
+              uint64_t ey;
               f2_split(tx, x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
+              const uint64_t ex = f2(ex2(x0), ex2(x1));
               if (!decltype(masked_t)::value && (re & 1)) {  // one pair in four on the FMA pipe
-                f2_split(exp2_poly2(ty), y0, y1);
+                ey = exp2_poly2(ty);
               } else {
                 f2_split(ty, y0, y1);
-                y0 = ex2(y0);
-                y1 = ex2(y1);
+                ey = f2(ex2(y0), ex2(y1));
               }
-              y0 *= nl.x;
-              y1 *= nl.y;
+              ey = mul2(ey, nl);
+              const uint64_t ww = add2(ex, ey);
+              f2_split(ex, x0, x1);
+              f2_split(ey, y0, y1);
               p1[hh][at] = __float_as_uint(x0), p1[hh][at + 1] = __float_as_uint(x1);
               p2[hh][at] = __float_as_uint(y0), p2[hh][at + 1] = __float_as_uint(y1);
-              w[hh][2 * j + e] = pack2<BF16>(x0 + y0, x1 + y1);
+              f2_split(ww, x0, x1);
+              w[hh][2 * j + e] = pack2<BF16>(x0, x1);
             }
           }
         };
@@ -696,12 +732,12 @@ __global__ void __launch_bounds__(448, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(w_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w_ready);
       // Phase B: dS_1 = p1 (dP - Delta_1), dS_2 = p2 (dP - Delta_2) in 16 bits,
       // into tensor memory over dP (the A operands of dK: 16 columns each) and
       // into swizzled shared memory (the A operands of dQ).
-      ok = __all_sync(0xffffffffu, wait_bar(dp_full, i & 1, abort_flag, kRoleSoftmax, i) &&
-                                       wait_bar(ds_free, ((i >> 1) & 1) ^ 1, abort_flag, kRoleSoftmax, i));
+      ok = __all_sync(0xffffffffu, wait_bar_c(dp_full, i & 1, abort_flag, kRoleSoftmax, i));
       if (!ok) break;
       tc_fence_after();
       uint32_t dp[2][16];
@@ -710,23 +746,30 @@ __global__ void __launch_bounds__(448, 1)
       tmem_ld_wait();
       reg_fence(dp[0]);
       reg_fence(dp[1]);
+      // (dP(i) was issued after the dQ products that last read these buffers.)
       const uint32_t row1 = smem_u32(smem + L::OFF_DS + (i & 1) * L::BLK) + kr * 128;
+      const uint32_t row2 = smem_u32(smem + L::OFF_DS2 + ((i & 1) ? 1 : (i & 2)) * L::BLK) + kr * 128;
       uint32_t d1[2][8], d2[2][8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 da = *reinterpret_cast<const float2*>(vec + 192 + 8 * j);
-        const float2 db = *reinterpret_cast<const float2*>(vec + 256 + 8 * j);
+        const uint64_t nda = *reinterpret_cast<const uint64_t*>(vec + 192 + 8 * j);
+        const uint64_t ndb = *reinterpret_cast<const uint64_t*>(vec + 256 + 8 * j);
 #pragma unroll
         for (int re = 0; re < 4; ++re) {
           const int hh = re >> 1, e = re & 1, at = 4 * j + 2 * e;
-          auto f = [](uint32_t x) { return __uint_as_float(x); };
-          const float g0 = f(dp[hh][at]), g1 = f(dp[hh][at + 1]);
-          d1[hh][2 * j + e] = pack2<BF16>(f(p1[hh][at]) * (g0 - da.x), f(p1[hh][at + 1]) * (g1 - da.y));
-          d2[hh][2 * j + e] = pack2<BF16>(f(p2[hh][at]) * (g0 - db.x), f(p2[hh][at + 1]) * (g1 - db.y));
+          auto two = [&](const uint32_t(&r)[2][16]) {
+            return f2(__uint_as_float(r[hh][at]), __uint_as_float(r[hh][at + 1]));
+          };
+          const uint64_t g2 = two(dp);
+          float x0, x1, y0, y1;
+          f2_split(mul2(two(p1), add2(g2, nda)), x0, x1);
+          f2_split(mul2(two(p2), add2(g2, ndb)), y0, y1);
+          d1[hh][2 * j + e] = pack2<BF16>(x0, x1);
+          d2[hh][2 * j + e] = pack2<BF16>(y0, y1);
         }
         const uint32_t sw = ((4 * g + j) ^ (kr & 7)) << 4;
         stsm_x4(row1 + sw, d1[0][2 * j], d1[0][2 * j + 1], d1[1][2 * j], d1[1][2 * j + 1]);
-        stsm_x4(row1 + 2 * L::BLK + sw, d2[0][2 * j], d2[0][2 * j + 1], d2[1][2 * j], d2[1][2 * j + 1]);
+        stsm_x4(row2 + sw, d2[0][2 * j], d2[0][2 * j + 1], d2[1][2 * j], d2[1][2 * j + 1]);
       }
       tmem_st_frag(tDP, d1[0]);
       tmem_st_frag(tDP + kUpper, d1[1]);
@@ -735,7 +778,8 @@ __global__ void __launch_bounds__(448, 1)
       tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(ds_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_ready);
     }
     // Epilogue: warpgroup 0 writes dK_c = scale * accumulator, warpgroup 1 dV.
     if (ok && !*abort_flag) {
@@ -780,10 +824,11 @@ __global__ void __launch_bounds__(448, 1)
     const int tr = wq * 32 + lane;  // TMEM lane = query row of the block
     const uint32_t tDQ = tmem + (static_cast<uint32_t>(wq * 32) << 16) + L::COL_DQ;
     for (int u = 0; u < n; ++u) {  // one use of the dQ buffer per map and block
-      if (!__all_sync(0xffffffffu, wait_bar(dq_full, u & 1, abort_flag, kRoleSoftmax, u))) break;
+      if (!__all_sync(0xffffffffu, wait_bar_c(dq_full, u & 1, abort_flag, kRoleSoftmax, u))) break;
       tc_fence_after();
       const int c = u & 1;
       const int bh = chunk_bh(u), r0 = chunk_row(u & ~1);
+      const int swap = (c & (u >> 1)) * 64;  // dQ_2 of an odd block: its halves have changed places
       uint32_t v[2][32];
       tmem_ld32(tDQ, v[0]);
       tmem_ld32(tDQ + 32, v[1]);
@@ -791,12 +836,13 @@ __global__ void __launch_bounds__(448, 1)
       reg_fence(v[0]);
       reg_fence(v[1]);
       tc_fence_before();
-      mbar_arrive(dq_free);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dq_free);
       if (a.dq_part != nullptr) {
         if (checked(bh < a.B * a.H && r0 / 128 < a.nqb && kvb < a.nkb, 513)) {
           float4* dst = reinterpret_cast<float4*>(
               a.dq_part +
-              (((static_cast<int64_t>(bh) * a.nqb + r0 / 128) * a.nkb + kvb) * 2 + c) * (128 * 64) + tr * 64);
+              (((static_cast<int64_t>(bh) * a.nqb + r0 / 128) * a.nkb + kvb) * 2 + c) * (128 * 64) + (tr ^ swap) * 64);
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -822,7 +868,7 @@ __global__ void __launch_bounds__(448, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            const int64_t row = c * acc_rows + static_cast<int64_t>(bh) * a.Sq_pad + r0 + 32 * wq;
+            const int64_t row = c * acc_rows + static_cast<int64_t>(bh) * a.Sq_pad + r0 + ((32 * wq) ^ swap);
             if (checked(row + 32 <= 2 * acc_rows, 514)) tma_reduce_add_2d(&tmDQ, buf, 32 * p, static_cast<int>(row));
             bulk_commit();
           }

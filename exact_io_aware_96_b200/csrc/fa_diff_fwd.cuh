@@ -66,6 +66,17 @@ __device__ __forceinline__ int diff_keys(const int* k_lens, int b, int Sk) {
   return k_lens == nullptr ? Sk : max(0, min(k_lens[b], Sk));
 }
 
+// wait_bar with everything after the first try out of line: the roles' loops
+// stay short enough to be fetched without a pause.
+__device__ __noinline__ bool wait_bar_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int role,
+                                           int iter) {
+  return wait_bar(bar, parity, abort_flag, role, iter);
+}
+__device__ __forceinline__ bool wait_bar_c(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int role,
+                                           int iter) {
+  return sm100::mbar_try_wait(bar, parity) || wait_bar_slow(bar, parity, abort_flag, role, iter);
+}
+
 template <int DV>
 struct DiffFwdLayout {
   static constexpr int kThreads = 576;
