@@ -104,6 +104,19 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Whether phase `parity` of `bar` has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(sm100::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The 64-bit descriptor of a 128-byte-swizzled operand from its low word
 // (address >> 4 and lbo >> 4 << 16); the high word is the same for all: 1024
 // bytes between 8-row groups, the sm_100 version and the swizzle mode.
@@ -325,21 +338,24 @@ struct DiffBwdLayout {
   static constexpr int BLK = 128 * 128;   // [128 rows][64 columns] of 16 bits
   static constexpr int HBLK = 64 * 128;   // [64 rows][64 columns]
   static constexpr int VB = DV / 64;
-  static constexpr int ST = 2;            // stages of (Q_1, Q_2, row terms) and of dO
+  // A stage of Q is in use from S(i) to dK(i), nearly two chunks; dO(i) is done
+  // with at dV(i), early enough for one stage.
+  static constexpr int QS = 3;            // stages of (Q_1, Q_2)
+  static constexpr int VS = 2;            // stages of the row terms
   static constexpr int OFF_K = 0;                       // K_1, K_2
   static constexpr int OFF_V = OFF_K + 2 * BLK;
   static constexpr int OFF_Q = OFF_V + VB * BLK;        // [stage][map][64 rows]
-  static constexpr int OFF_DO = OFF_Q + ST * 2 * HBLK;  // [stage][column block][64 rows]
-  static constexpr int OFF_DS = OFF_DO + ST * VB * HBLK;  // dS_1^T: [chunk half][128 keys][64 queries]
+  static constexpr int OFF_DO = OFF_Q + QS * 2 * HBLK;  // [column block][64 rows]
+  static constexpr int OFF_DS = OFF_DO + VB * HBLK;  // dS_1^T: [chunk half][128 keys][64 queries]
   // dS_2^T's first half alternates between blocks 0 and 2, so that dQ_2 of a
   // block may still read its dS while the next block's is written.
   static constexpr int OFF_DS2 = OFF_DS + 2 * BLK;
   static constexpr int OFF_DQS = OFF_DS2 + 3 * BLK;     // dQ staging: 4 KB per drain warp
   static constexpr int OFF_VEC = OFF_DQS + 4 * 4096;
-  static constexpr int OFF_BAR = OFF_VEC + ST * kDiffVec * 4;
-  // kv_full, q_full/q_empty[ST], o_full/o_empty[ST], s_full, w_ready, dp_full, ds_ready, dq_full, dq_free,
-  // mma_done, drain
-  static constexpr int NBAR = 1 + 4 * ST + 8;
+  static constexpr int OFF_BAR = OFF_VEC + VS * kDiffVec * 4;
+  // kv_full, q_full/q_empty[QS], v_full[VS], o_full, o_empty, s_full, w_ready, dp_full, ds_ready, dq_full,
+  // dq_free, mma_done, drain
+  static constexpr int NBAR = 1 + 2 * QS + VS + 10;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM_MAX = 232448;
@@ -362,8 +378,7 @@ __global__ void __launch_bounds__(448, 1)
                      const __grid_constant__ CUtensorMap tmDQ, const DiffBwdArgs a) {
   using L = DiffBwdLayout<DV>;
   using namespace sm100;
-  constexpr int ST = L::ST;
-  static_assert(ST == 2, "the MMA warp unrolls its loop by the stages");
+  constexpr int QS = L::QS, VS = L::VS;
   static_assert(L::BYTES <= L::SMEM_MAX, "smem budget");
 
   extern __shared__ uint8_t smem_raw[];
@@ -377,10 +392,11 @@ __global__ void __launch_bounds__(448, 1)
   const int lane = threadIdx.x & 31;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* q_full = kv_full + 1;
-  uint64_t* q_empty = q_full + ST;
-  uint64_t* o_full = q_empty + ST;
-  uint64_t* o_empty = o_full + ST;
-  uint64_t* s_full = o_empty + ST;
+  uint64_t* q_empty = q_full + QS;
+  uint64_t* v_full = q_empty + QS;
+  uint64_t* o_full = v_full + VS;
+  uint64_t* o_empty = o_full + 1;
+  uint64_t* s_full = o_empty + 1;
   uint64_t* w_ready = s_full + 1;
   uint64_t* dp_full = w_ready + 1;
   uint64_t* ds_ready = dp_full + 1;
@@ -414,12 +430,13 @@ __global__ void __launch_bounds__(448, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < QS; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
-      mbar_init(&o_full[s], 1);
-      mbar_init(&o_empty[s], 1);
     }
+    for (int s = 0; s < VS; ++s) mbar_init(&v_full[s], 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 1);
     mbar_init(s_full, 1);
     mbar_init(w_ready, 8);  // one arrival per softmax warp
     mbar_init(dp_full, 1);
@@ -457,41 +474,38 @@ __global__ void __launch_bounds__(448, 1)
       tma_load_4d(smem + L::OFF_K + L::BLK, &tmK2, kv_full, 0, n0, hk, b);
       for (int vb = 0; vb < L::VB; ++vb)
         tma_load_4d(smem + L::OFF_V + vb * L::BLK, &tmV, kv_full, vb * 64, n0, hk, b);
-      int nq = 0, no = 0;  // loads issued
-      auto load_q = [&](int i) -> bool {
-        const int st = i % ST;
-        if (!wait_bar(&q_empty[st], ((i / ST) & 1) ^ 1, abort_flag, kRoleLoader, i)) return false;
+      int nq = 0, nv = 0, no = 0;  // loads issued
+      auto load = [&](int i) -> bool {
+        const int qs = i % QS, vs = i % VS;
         const int bh = chunk_bh(i), r0 = chunk_row(i), h = bh - b * a.H;
-        mbar_arrive_expect_tx(&q_full[st], 2 * L::HBLK + kDiffVec * 4);
-        tma_load_4d(smem + L::OFF_Q + st * 2 * L::HBLK, &tmQ1, &q_full[st], 0, r0, h, b);
-        tma_load_4d(smem + L::OFF_Q + (st * 2 + 1) * L::HBLK, &tmQ2, &q_full[st], 0, r0, h, b);
+        // Row terms: free once the softmax warps are through with chunk i - 2.
+        if (i >= VS && !wait_bar(ds_ready, (i - VS) & 1, abort_flag, kRoleLoader, i)) return false;
+        mbar_arrive_expect_tx(&v_full[vs], kDiffVec * 4);
         // Skipped on a failed check: its wait then runs out (FA_ERR_BOUNDS stays recorded).
         if (checked(r0 + 64 <= a.Sq_pad && h < a.H, 511))
-          bulk_load(smem + L::OFF_VEC + st * kDiffVec * 4,
+          bulk_load(smem + L::OFF_VEC + vs * kDiffVec * 4,
                     a.vec + (static_cast<int64_t>(bh) * (a.Sq_pad / 64) + r0 / 64) * kDiffVec, kDiffVec * 4,
-                    &q_full[st]);
+                    &v_full[vs]);
+        ++nv;
+        if (!wait_bar(&q_empty[qs], ((i / QS) & 1) ^ 1, abort_flag, kRoleLoader, i)) return false;
+        mbar_arrive_expect_tx(&q_full[qs], 2 * L::HBLK);
+        tma_load_4d(smem + L::OFF_Q + qs * 2 * L::HBLK, &tmQ1, &q_full[qs], 0, r0, h, b);
+        tma_load_4d(smem + L::OFF_Q + (qs * 2 + 1) * L::HBLK, &tmQ2, &q_full[qs], 0, r0, h, b);
         ++nq;
-        return true;
-      };
-      auto load_o = [&](int i) -> bool {
-        const int st = i % ST;
-        if (!wait_bar(&o_empty[st], ((i / ST) & 1) ^ 1, abort_flag, kRoleLoader, i)) return false;
-        const int h = chunk_bh(i) - b * a.H, r0 = chunk_row(i);
-        mbar_arrive_expect_tx(&o_full[st], L::VB * L::HBLK);
+        if (!wait_bar(o_empty, (i & 1) ^ 1, abort_flag, kRoleLoader, i)) return false;
+        mbar_arrive_expect_tx(o_full, L::VB * L::HBLK);
         for (int vb = 0; vb < L::VB; ++vb)
-          tma_load_4d(smem + L::OFF_DO + (st * L::VB + vb) * L::HBLK, &tmdO, &o_full[st], vb * 64, r0, h, b);
+          tma_load_4d(smem + L::OFF_DO + vb * L::HBLK, &tmdO, o_full, vb * 64, r0, h, b);
         ++no;
         return true;
       };
-      bool lok = true;
-      for (int i = 0; lok && i < n; ++i) {
-        lok = load_o(i);  // a stage of dO frees before the same chunk's stage of Q
-        if (lok) lok = load_q(i);
+      for (int i = 0; i < n && load(i); ++i) {
       }
       if (*abort_flag) {
         drain_wait(kv_full, 0);
-        for (int i = max(0, nq - ST); i < nq; ++i) drain_wait(&q_full[i % ST], (i / ST) & 1);
-        for (int i = max(0, no - ST); i < no; ++i) drain_wait(&o_full[i % ST], (i / ST) & 1);
+        for (int i = max(0, nq - QS); i < nq; ++i) drain_wait(&q_full[i % QS], (i / QS) & 1);
+        for (int i = max(0, nv - VS); i < nv; ++i) drain_wait(&v_full[i % VS], (i / VS) & 1);
+        if (no > 0) drain_wait(o_full, (no - 1) & 1);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -507,48 +521,45 @@ __global__ void __launch_bounds__(448, 1)
       constexpr uint32_t id_k = idesc_f16(BF16, 128, 64, 0, 1);
       // dQ_c = dS_c K_c: M = 128 queries, N = 64, K = 128 keys; A = dS_c^T viewed MN-major, B = K_c MN-major.
       constexpr uint32_t id_q = idesc_f16(BF16, 128, 64, 1, 1);
-      // Operand descriptors differ in their low words only (address and lbo), by
-      // constants once the stage is one: the chunk loop is unrolled by the two
-      // stages, and every operand is one addition away. The issuing warp's own
-      // instructions, not the tensor core, were what a chunk waited for before
-      // (490 -> 4xx us at S = 8192).
+      // Operand descriptors differ in their low words only (address and lbo):
+      // every operand is one addition away.
       const uint32_t base = smem_u32(smem) >> 4;
       auto desc = [&](uint32_t off, uint32_t lbo) { return desc_words(base + (off >> 4) + ((lbo >> 4) << 16)); };
-      auto issue_S = [&](int st) {
+      auto issue_S = [&](int qs) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint64_t ad[4], bd[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             ad[u] = desc(L::OFF_K + c * L::BLK + u * 32, 16);
-            bd[u] = desc(L::OFF_Q + (st * 2 + c) * L::HBLK + u * 32, 16);
+            bd[u] = desc(L::OFF_Q + (qs * 2 + c) * L::HBLK + u * 32, 16);
           }
           mma_ss_x4(tmem + L::COL_S + 64 * c, ad, bd, id_s, 0);
         }
       };
-      auto issue_dP = [&](int st) {
+      auto issue_dP = [&]() {
 #pragma unroll
         for (int vb = 0; vb < L::VB; ++vb) {
           uint64_t ad[4], bd[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             ad[u] = desc(L::OFF_V + vb * L::BLK + u * 32, 16);
-            bd[u] = desc(L::OFF_DO + (st * L::VB + vb) * L::HBLK + u * 32, 16);
+            bd[u] = desc(L::OFF_DO + vb * L::HBLK + u * 32, 16);
           }
           mma_ss_x4(tmem + L::COL_DP, ad, bd, id_s, vb > 0);
         }
       };
-      auto issue_dV = [&](int st, uint32_t acc) {
+      auto issue_dV = [&](uint32_t acc) {
         uint32_t pa[4];
         uint64_t bd[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           pa[u] = tmem + L::COL_S + (u >> 1) * 32 + (u & 1) * 8;  // W^T of queries 16u .. 16u + 15
-          bd[u] = desc(L::OFF_DO + st * L::VB * L::HBLK + u * 2048, L::HBLK);
+          bd[u] = desc(L::OFF_DO + u * 2048, L::HBLK);
         }
         mma_ts_x4(tmem + L::COL_DV, pa, bd, id_v, acc);
       };
-      auto issue_dK = [&](int st, uint32_t acc) {
+      auto issue_dK = [&](int qs, uint32_t acc) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pa[4];
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(448, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             pa[u] = tmem + L::COL_DP + (u >> 1) * 32 + 16 * c + (u & 1) * 8;  // dS_c^T of queries 16u .. 16u + 15
-            bd[u] = desc(L::OFF_Q + (st * 2 + c) * L::HBLK + u * 2048, L::HBLK);
+            bd[u] = desc(L::OFF_Q + (qs * 2 + c) * L::HBLK + u * 2048, L::HBLK);
           }
           mma_ts_x4(tmem + L::COL_DK + 64 * c, pa, bd, id_k, acc);
         }
@@ -582,52 +593,59 @@ __global__ void __launch_bounds__(448, 1)
         tc_fence_after();
         issue_S(0);
         mma_commit_w(s_full);
-        ok = wait(&o_full[0], 0, 0);
+        ok = wait(o_full, 0, 0);
       }
       if (ok) {
         tc_fence_after();
-        issue_dP(0);
+        issue_dP();
         mma_commit_w(dp_full);
       }
-      // Chunk i = 2 blk + st (the number of chunks is even and ST is 2, so a
-      // chunk's stage is its half of the block, and q_full, o_full have
-      // completed blk times before).
-      auto chunk = [&](int blk, auto half) -> bool {
-        constexpr int st = decltype(half)::value, sn = st ^ 1;
-        const int i = 2 * blk + st;
-        const uint32_t phn = (blk + st) & 1;  // phase of chunk i + 1's loads
+      int qs = 0;             // Q's stage of the chunk
+      uint32_t q_phase = 0;   // and its phase
+      auto chunk = [&](int blk, auto half) -> bool {  // chunk i = 2 blk + half
+        constexpr int hf = decltype(half)::value;
+        const int i = 2 * blk + hf;
         const bool more = i + 1 < n;
-        if (!wait(w_ready, st, i)) return false;
+        const int qn = qs == QS - 1 ? 0 : qs + 1;
+        const uint32_t q_phase_n = q_phase ^ (qn == 0);
+        if (!wait(w_ready, hf, i)) return false;
+        // The loads and the drain that the products below need are looked at
+        // ahead of them: a wait between two groups of products, even for what is
+        // there, lets the tensor core run dry (476 -> 468 us at S = 8192).
+        const bool q_in = mbar_test(&q_full[qn], q_phase_n), dq_out = mbar_test(dq_free, hf);
         tc_fence_after();
-        issue_dV(st, i > 0);
-        mma_commit_w(&o_empty[st]);  // dP(i), issued before, and dV(i) are dO(i)'s readers
+        issue_dV(i > 0);
+        mma_commit_w(o_empty);  // dP(i), issued before, and dV(i) are dO(i)'s readers
         if (more) {
           // S(i+1) goes over S(i) and W(i): the softmax warps have read S(i)
           // (w_ready) and dV(i), issued before, reads W(i) first.
-          if (!wait(&q_full[sn], phn, i + 1)) return false;
-          issue_S(sn);
+          if (!__all_sync(0xffffffffu, q_in) && !wait(&q_full[qn], q_phase_n, i + 1)) return false;
+          issue_S(qn);
           mma_commit_w(s_full);
         }
-        if (st == 0 && blk > 0) {
+        if (hf == 0 && blk > 0) {
           // dQ_2 of the block before, once dQ_1 has been drained.
-          if (!wait(dq_free, 0, i)) return false;
+          if (!__all_sync(0xffffffffu, dq_out) && !wait(dq_free, 0, i)) return false;
           tc_fence_after();
           issue_dQ(1, (blk - 1) & 1);
         }
-        if (!wait(ds_ready, st, i)) return false;
+        if (!wait(ds_ready, hf, i)) return false;
+        const bool o_in = mbar_test(o_full, hf ^ 1);
         tc_fence_after();
-        if (st) {
-          if (blk > 0 && !wait(dq_free, 1, i)) return false;  // the block before's dQ_2 has been drained
+        if (hf) {
+          if (blk > 0 && !__all_sync(0xffffffffu, dq_out) && !wait(dq_free, 1, i)) return false;  // the block before's dQ_2 has been drained
           tc_fence_after();
           issue_dQ(0, 0);
         }
-        issue_dK(st, i > 0);
-        mma_commit_w(&q_empty[st]);
+        issue_dK(qs, i > 0);
+        mma_commit_w(&q_empty[qs]);
         if (more) {
-          if (!wait(&o_full[sn], phn, i + 1)) return false;
-          issue_dP(sn);
+          if (!__all_sync(0xffffffffu, o_in) && !wait(o_full, hf ^ 1, i + 1)) return false;
+          issue_dP();
           mma_commit_w(dp_full);
         }
+        qs = qn;
+        q_phase = q_phase_n;
         return true;
       };
       const int blocks = n / 2;
@@ -655,16 +673,16 @@ __global__ void __launch_bounds__(448, 1)
     const float sl2 = a.scale_log2;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int st = i % ST;
+      const int vs = i % VS;
       ok = __all_sync(0xffffffffu, wait_bar_c(s_full, i & 1, abort_flag, kRoleSoftmax, i) &&
-                                       wait_bar_c(&q_full[st], (i / ST) & 1, abort_flag, kRoleSoftmax, i));
+                                       wait_bar_c(&v_full[vs], (i / VS) & 1, abort_flag, kRoleSoftmax, i));
       if (!ok) break;
       tc_fence_after();
       // Query column e of this warpgroup's 32 is masked for key k if e < k + cm0
       // (causal), or if k is past the end.
       const int cm0 = a.causal ? n0 + wq * 32 - off - chunk_row(i) - 32 * g : -256;
       const bool masked = cm0 + 31 > 0 || n0 + wq * 32 + 31 >= a.Sk;
-      const float* vec = s_vec + st * kDiffVec + 32 * g + fc;
+      const float* vec = s_vec + vs * kDiffVec + 32 * g + fc;
       // Phase A: p1 = P_1^T, p2 = -lambda P_2^T (fp32, kept), W^T = p1 + p2 in
       // 16 bits over S_1^T.
       uint32_t p1[2][16], p2[2][16];
