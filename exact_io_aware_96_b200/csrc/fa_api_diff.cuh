@@ -321,14 +321,27 @@ int launch_rotary(const fa_rotary_params* p, cudaStream_t stream) {
   for (int i = 0; i < p->axes; ++i) a.R += p->sections[i], a.end[i] = a.R;
   a.B = p->B, a.S = p->S, a.D = p->D;
   a.sign = p->inverse ? -1.f : 1.f;
-  // Tokens per block: about 16 KB of q and k, while the grid still covers the
-  // SMs; the sines and cosines stay within 16 KB.
+  // Work items: pairs in groups of VEC, the largest power of two up to 8 that
+  // divides R, so that both halves of a group are aligned (interleaved: 8
+  // columns, four pairs); then the copied columns.
+  const int vec = p->interleaved || a.R % 8 == 0 ? 8 : a.R % 4 == 0 ? 4 : a.R % 2 == 0 ? 2 : 1;
+  a.n_rot = p->interleaved ? (2 * a.R + 7) / 8 : a.R / vec;
+  a.n_item = p->interleaved ? a.D / 8 : a.n_rot + (a.D - 2 * a.R) / vec;
+  const int64_t per_tok = int64_t(p->H + p->Hk) * a.n_item;
+  a.per_tok = int(per_tok);
+  // Tokens per block: up to 1024 items, the four per thread whose loads go out
+  // before the angles are computed, while the grid still covers the SMs; the
+  // sines and cosines stay within 16 KB.
   const int64_t total = int64_t(p->B) * p->S;
-  const int64_t row_bytes = int64_t(p->H + p->Hk) * p->D * 2;
-  int64_t tokens = std::max<int64_t>(1, 16384 / row_bytes);
+  int64_t tokens = std::max<int64_t>(1, 1024 / per_tok);
   tokens = std::min<int64_t>(tokens, std::max<int64_t>(1, 2048 / a.R));
   tokens = std::min<int64_t>(tokens, std::max<int64_t>(1, total / 592));
+  // (Divisions by reciprocals: items * per_tok below 2^32; see div_by.)
+  tokens = std::min<int64_t>({tokens, fa::kRotMaxTokens, std::max<int64_t>(1, 0xffffffffll / (per_tok * per_tok))});
   a.tokens = int(tokens);
+  auto inverse = [](int64_t d) { return d == 1 ? 0u : uint32_t((uint64_t(1) << 32) / uint64_t(d) + 1); };
+  a.inv_item = inverse(a.n_item);
+  a.inv_tok = tokens == 1 ? 1u : inverse(per_tok);  // 1 gives 0 for every item
   const unsigned grid = unsigned((total + tokens - 1) / tokens);
   const int smem = int(tokens) * a.R * int(sizeof(float2));
   auto go = [&](auto* kern) {
@@ -336,9 +349,9 @@ int launch_rotary(const fa_rotary_params* p, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   };
   if (p->interleaved) return go(&fa::fa_rotary_kernel<BF16, true, 8>);
-  if (a.R % 8 == 0) return go(&fa::fa_rotary_kernel<BF16, false, 8>);
-  if (a.R % 4 == 0) return go(&fa::fa_rotary_kernel<BF16, false, 4>);
-  if (a.R % 2 == 0) return go(&fa::fa_rotary_kernel<BF16, false, 2>);
+  if (vec == 8) return go(&fa::fa_rotary_kernel<BF16, false, 8>);
+  if (vec == 4) return go(&fa::fa_rotary_kernel<BF16, false, 4>);
+  if (vec == 2) return go(&fa::fa_rotary_kernel<BF16, false, 2>);
   return go(&fa::fa_rotary_kernel<BF16, false, 1>);
 }
 
@@ -415,7 +428,7 @@ int fa_rotary(const fa_rotary_params* p, fa_stream_t stream) {
   if (p->dtype != FA_FP16 && p->dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
   if (p->D < 8 || p->D > 256 || p->D % 8) return FA_ERR_UNSUPPORTED;
   const int64_t lim = (int64_t(1) << 31) - 1;
-  if (int64_t(p->B) * p->S > lim || int64_t(p->H) + p->Hk > 65536) return FA_ERR_INVALID_ARG;
+  if (int64_t(p->B) * p->S > lim || int64_t(p->H) + p->Hk > 4095) return FA_ERR_INVALID_ARG;
   if (p->axes < 1 || p->axes > FA_ROTARY_MAX_AXES) return FA_ERR_INVALID_ARG;
   int64_t pairs = 0;
   for (int i = 0; i < p->axes; ++i) {

@@ -401,7 +401,7 @@ typedef struct {
   int inv_freq_fp64;      /* 0: fp32, 1: fp64 */
   int axes;               /* 1 .. FA_ROTARY_MAX_AXES */
   int sections[FA_ROTARY_MAX_AXES]; /* pairs of each axis, >= 0; 1 <= R <= D / 2 */
-  int B, S, H, Hk, D;     /* D a multiple of 8 in [8, 256]; Hk >= 0 */
+  int B, S, H, Hk, D;     /* D a multiple of 8 in [8, 256]; Hk >= 0; H + Hk <= 4095 */
   int interleaved, inverse;
   int dtype;              /* FA_FP16 or FA_BF16 */
 } fa_rotary_params;
