@@ -96,6 +96,8 @@ class PackedQKVAttention(torch.nn.Module):
 
 def _strided_ready(t: torch.Tensor) -> torch.Tensor:
     """`t`, or a dense copy if its strides, alignment or an expanded axis keep the kernels from reading it."""
+    if t.data_ptr() % 16 == 0 and t.is_contiguous():
+        return t
     ok = (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
           and all(s % 8 == 0 and (s > 0 or n == 1) for s, n in zip(t.stride()[:-1], t.shape[:-1])))
     return t if ok else t.clone(memory_format=torch.contiguous_format)

@@ -221,8 +221,8 @@ int launch_lam(const fa_diff_bwd_params* p, const float* drow, float* part, cuda
   a.ext[0] = p->lambda.extent_b, a.ext[1] = p->lambda.extent_s, a.ext[2] = p->lambda.extent_h;
   a.n_out = int64_t(a.ext[0]) * a.ext[1] * a.ext[2];
   a.count = int64_t(a.B) * a.H * a.Sq / a.n_out;
-  if (a.count == 1) {
-    fa::fa_diff_lam_copy<<<unsigned((a.n_out + 255) / 256), 256, 0, stream>>>(a);
+  if (a.count <= 32) {
+    fa::fa_diff_lam_few<<<unsigned((a.n_out + 255) / 256), 256, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   }
   // Long sums of few elements are cut into runs of 2048 terms or more, at most
@@ -329,11 +329,11 @@ int launch_rotary(const fa_rotary_params* p, cudaStream_t stream) {
   a.n_item = p->interleaved ? a.D / 8 : a.n_rot + (a.D - 2 * a.R) / vec;
   const int64_t per_tok = int64_t(p->H + p->Hk) * a.n_item;
   a.per_tok = int(per_tok);
-  // Tokens per block: up to 1024 items, the four per thread whose loads go out
+  // Tokens per block: up to 2048 items, of which four per thread have their loads go out
   // before the angles are computed, while the grid still covers the SMs; the
   // sines and cosines stay within 16 KB.
   const int64_t total = int64_t(p->B) * p->S;
-  int64_t tokens = std::max<int64_t>(1, 1024 / per_tok);
+  int64_t tokens = std::max<int64_t>(1, 2048 / per_tok);
   tokens = std::min<int64_t>(tokens, std::max<int64_t>(1, 2048 / a.R));
   tokens = std::min<int64_t>(tokens, std::max<int64_t>(1, total / 592));
   // (Divisions by reciprocals: items * per_tok below 2^32; see div_by.)

@@ -20,7 +20,7 @@
 //     of shared heads are summed in the CTA's fp32 accumulators, in a fixed
 //     order.
 //  3. fa_diff_dq: dq_c = scale * accumulator, rounded to the input dtype.
-//  4. fa_diff_lam_part / fa_diff_lam_sum: dlambda, summed over the axes lambda
+//  4. fa_diff_lam_few, or fa_diff_lam_part and fa_diff_lam_sum: dlambda, summed over the axes lambda
 //     is broadcast over in a fixed order.
 //
 // Main kernel. Query rows go through the softmax 64 at a time ("chunks", two
@@ -287,33 +287,34 @@ __device__ __forceinline__ void store_lam(void* p, int kind, int64_t at, float v
         static_cast<uint16_t>((kind == kLamBF16 ? sm100::pack2<true>(v, 0.f) : sm100::pack2<false>(v, 0.f)) & 0xffffu);
 }
 
-// No axis is broadcast: one thread per element.
-__global__ void __launch_bounds__(256) fa_diff_lam_copy(const LamSumArgs a) {
-  const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // [B][Sq][H]
+// Term k of element x's sum. The summed axes, innermost first: rows, heads, batch.
+__device__ __forceinline__ float lam_term(const LamSumArgs& a, int64_t x, int64_t k) {
+  const int eh = static_cast<int>(x % a.ext[2]);
+  const int64_t y = x / a.ext[2];
+  const int es = static_cast<int>(y % a.ext[1]), eb = static_cast<int>(y / a.ext[1]);
+  const int ns = a.ext[1] == 1 ? a.Sq : 1, nh = a.ext[2] == 1 ? a.H : 1;
+  const int64_t s = k % ns, z = k / ns;
+  const int64_t h = z % nh, b = z / nh;
+  return a.drow[((eb + b) * a.H + eh + h) * a.Sq + es + s];
+}
+
+// Few terms (one, where no axis is broadcast): one thread per element.
+__global__ void __launch_bounds__(256) fa_diff_lam_few(const LamSumArgs a) {
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (x >= a.n_out) return;
-  const int h = static_cast<int>(x % a.H);
-  const int64_t bs = x / a.H;
-  const int64_t b = bs / a.Sq, s = bs - b * a.Sq;
-  store_lam(a.dlam, a.dlam_kind, x, a.drow[(b * a.H + h) * a.Sq + s]);
+  float v = 0.f;
+  for (int64_t k = 0; k < a.count; ++k) v += lam_term(a, x, k);
+  store_lam(a.dlam, a.dlam_kind, x, v);
 }
 
 __global__ void __launch_bounds__(256) fa_diff_lam_part(const LamSumArgs a) {
   __shared__ float sm[8];
   const int64_t x = blockIdx.x / a.parts;
   const int run = static_cast<int>(blockIdx.x % a.parts);
-  const int eh = static_cast<int>(x % a.ext[2]);
-  const int64_t y = x / a.ext[2];
-  const int es = static_cast<int>(y % a.ext[1]), eb = static_cast<int>(y / a.ext[1]);
-  // The summed axes, innermost first: rows, heads, batch.
-  const int ns = a.ext[1] == 1 ? a.Sq : 1, nh = a.ext[2] == 1 ? a.H : 1;
   const int64_t len = (a.count + a.parts - 1) / a.parts;
   const int64_t lo = run * len, hi = min(a.count, lo + len);
   float v = 0.f;
-  for (int64_t k = lo + threadIdx.x; k < hi; k += 256) {
-    const int64_t s = k % ns, z = k / ns;
-    const int64_t h = z % nh, b = z / nh;
-    v += a.drow[((eb + b) * a.H + eh + h) * a.Sq + es + s];
-  }
+  for (int64_t k = lo + threadIdx.x; k < hi; k += 256) v += lam_term(a, x, k);
   v = block_sum<256>(v, sm);
   if (threadIdx.x == 0) {
     if (a.parts == 1)

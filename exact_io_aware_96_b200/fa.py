@@ -544,8 +544,11 @@ def _elsewhere(dev, stream) -> bool:
     return stream is not None or dev.index != torch.cuda.current_device()
 
 
-def _current(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+try:  # the handle alone, without a Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:  # a torch without CUDA, or without this function
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _flat(name: str, t: torch.Tensor):
@@ -635,18 +638,18 @@ def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=Fa
             raise ValueError("k_lens must be contiguous")
     shape, causal = (B, Sq, H, Dv), 1 if causal else 0
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        out = q.new_empty(shape)
     else:
         _need("out", out, shape, q.dtype, dev)
     if out2 is not None:
         _need("out2", out2, shape, q.dtype, dev)
     elif need_o2:
-        out2 = torch.empty(shape, dtype=q.dtype, device=dev)
+        out2 = q.new_empty(shape)
     if lse is None:
         lse = torch.empty((2, B, H, Sq), dtype=torch.float32, device=dev)
     else:
         _diff_lse(lse, B, H, Sq, dev)
-    if workspace is None:
+    if workspace is None and Sq <= 16:  # calls of more rows need none
         n = fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal)
         workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     p = _DIFF_FWD.pack(*_pair("q", q), *_pair("k", k), *_flat("v", v), *lp,
@@ -654,7 +657,7 @@ def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=Fa
                        *(_NO_TENSOR if out2 is None else _flat("out2", out2)), lse.data_ptr(),
                        B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale), causal, dt,
                        *_ws(workspace, dev))
-    st = _packed("fa_diff_fwd")(p, _current(dev))
+    st = _packed("fa_diff_fwd")(p, _raw_stream(dev.index))
     if st != FA_OK:
         raise FaError(st, "fa_diff_fwd")
     return out, lse, out2
@@ -676,12 +679,14 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=Non
     for name, t in (("o", o), ("o2", o2), ("do", do)):
         _need(name, t, shape, q.dtype, dev)
     _diff_lse(lse, B, H, Sq, dev)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=q.dtype, device=dev) if dv is None else dv
-    dlam = torch.empty(lam.shape, dtype=lam.dtype, device=dev) if dlam is None else dlam
+    grads = []
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dlam", dlam, lam)):
-        _need(name, t, like.shape, like.dtype, dev)
+        if t is None:
+            t = like.new_empty(like.shape)
+        else:
+            _need(name, t, like.shape, like.dtype, dev)
+        grads.append(t)
+    dq, dk, dv, dlam = grads
     if not dlam.is_contiguous():
         raise ValueError("dlam must be contiguous")
     if workspace is None:
@@ -690,7 +695,7 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=Non
                        *_flat("do", do), lse.data_ptr(), *lp, *_pair("dq", dq), *_pair("dk", dk), *_flat("dv", dv),
                        dlam.data_ptr(), B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale),
                        1 if causal else 0, dt, *_ws(workspace, dev), det)
-    st = _packed("fa_diff_bwd")(p, _current(dev))
+    st = _packed("fa_diff_bwd")(p, _raw_stream(dev.index))
     if st != FA_OK:
         raise FaError(st, "fa_diff_bwd")
     return dq, dk, dv, dlam
@@ -760,7 +765,7 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
     if 2 * pairs > D:
         raise ValueError(f"{pairs} pairs do not fit into {D} columns")
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=dtype, device=dev)
+        out_q = q.new_empty(q.shape)
     elif out_q.shape != q.shape:
         _expect("out_q", out_q, q.shape, dtype, dev)
     if k is None:
@@ -769,7 +774,7 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
         wk = _NO_TENSOR
     else:
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=dtype, device=dev)
+            out_k = k.new_empty(k.shape)
         elif out_k.shape != k.shape:
             _expect("out_k", out_k, k.shape, dtype, dev)
         wk = _heads("out_k", out_k, B, S, D, dtype, dev)[1]
@@ -778,7 +783,7 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
                      1 if inv_freq.dtype is torch.float64 else 0, axes,
                      *sections, *(0,) * (FA_ROTARY_MAX_AXES - axes), B, S, H, Hk, D,
                      1 if interleaved else 0, 1 if inverse else 0, dt)
-    st = _packed("fa_rotary")(p, _current(dev))
+    st = _packed("fa_rotary")(p, _raw_stream(dev.index))
     if st != FA_OK:
         raise FaError(st, "fa_rotary")
     return out_q, out_k

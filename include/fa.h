@@ -364,9 +364,9 @@ typedef struct {
 /* Forward. */
 int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream);
 
-/* Workspace bytes of fa_diff_fwd on the current device (0 for most shapes;
-   calls of few query rows over many keys split the keys over the SMs and
-   need some). Host only. 0 also for arguments that fa_diff_fwd refuses. */
+/* Workspace bytes of fa_diff_fwd on the current device (0 for Sq > 16 and
+   other shapes; calls of few query rows over many keys split the keys over the
+   SMs and need some). Host only. 0 also for arguments that fa_diff_fwd refuses. */
 size_t fa_diff_fwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, int causal);
 
 /* Backward of L = sum(dO * O). The forward must have attended to all Sk keys
