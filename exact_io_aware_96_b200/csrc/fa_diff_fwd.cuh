@@ -33,6 +33,8 @@
 // FMA pipe).
 #pragma once
 
+#include <type_traits>
+
 #include "fa_common.cuh"
 #include "fa_fwd.cuh"
 
@@ -303,91 +305,88 @@ __global__ void __launch_bounds__(576, 1)
       int lim = sk - 1 - k0;  // last allowed column of this half
       if (a.causal) lim = min(lim, row + off - k0);
       float* slot = pmax + (((j & 1) * 2 + t) * 2) * 128;
-      float pm = -INFINITY;
+      const uint64_t sl2x2 = f2(sl2, sl2);
+      float pm = -INFINITY, add = 0.f;
+      uint32_t pw[2][16];  // P, two keys to a word
+      bool keep = ready;
+      // P, its sum and the row's maximum in one pass over this half's S, 32
+      // columns at a time, with the maximum of the blocks before.
+      auto pass = [&](auto masked_t) {
+        constexpr bool M = decltype(masked_t)::value;
+        const float mu = (m == -INFINITY) ? 0.f : m;
+        const uint64_t negmu2 = f2(-mu, -mu);
+        uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t sv[32];
+          tmem_ld32(tS + 32 * q, sv);
+          tmem_ld_wait();
+          reg_fence(sv);
+          auto xf = [&](int i) {
+            const float x = __uint_as_float(sv[i]);
+            return !M || 32 * q + i <= lim ? x : -INFINITY;
+          };
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            mx0 = max3(mx0, xf(i), xf(i + 1));
+            mx1 = max3(mx1, xf(i + 2), xf(i + 3));
+            mx2 = max3(mx2, xf(i + 4), xf(i + 5));
+            mx3 = max3(mx3, xf(i + 6), xf(i + 7));
+          }
+          fwd_exp32<BF16, M>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
+        }
+        pm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        float a0, a1;
+        f2_split(add2(acc0, acc1), a0, a1);
+        add = a0 + a1;
+      };
       if (ready) {
         tc_fence_after();
-        uint32_t rr[2][32];
-        tmem_ld32(tS, rr[0]);
-        tmem_ld32(tS + 32, rr[1]);
-        tmem_ld_wait();
-        reg_fence(rr[0]);
-        reg_fence(rr[1]);
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              rr[q][i] = (32 * q + i <= lim) ? rr[q][i] : __float_as_uint(-INFINITY);
-        }
-        auto xf = [&](int i) { return __uint_as_float(rr[i >> 5][i & 31]); };
-        float mx0 = max3(xf(0), xf(1), xf(2)), mx1 = max3(xf(3), xf(4), xf(5));
-        float mx2 = max3(xf(6), xf(7), xf(8)), mx3 = max3(xf(9), xf(10), xf(11));
-#pragma unroll
-        for (int i = 12; i < 60; i += 8) {
-          mx0 = max3(mx0, xf(i), xf(i + 1));
-          mx1 = max3(mx1, xf(i + 2), xf(i + 3));
-          mx2 = max3(mx2, xf(i + 4), xf(i + 5));
-          mx3 = max3(mx3, xf(i + 6), xf(i + 7));
-        }
-        mx0 = max3(mx0, xf(60), xf(61));
-        mx1 = max3(mx1, xf(62), xf(63));
-        pm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        if (masked)
+          pass(std::true_type{});
+        else
+          pass(std::false_type{});
         // Written again in block j + 2, after the partner has passed the
         // barrier of block j + 1, i.e. after it has read this value.
         slot[c * 128 + r] = pm;
+        keep = !(pm * sl2 > m + 8.0f);
       }
-      if (!named_bar_and(pair_bar, 64, ready)) {
-        ok = false;
-        break;
-      }
-      const float m_blk = fmaxf(pm, slot[(c ^ 1) * 128 + r]) * sl2;
-      const bool raise = m_blk > m + 8.0f;
-      float alpha = 1.f;
-      if (raise) {
-        alpha = ex2(m - m_blk);  // 0 when m was -inf
-        m = m_blk;
-      }
-      l *= alpha;
-      // S_t(j) was issued after P_t(j-1) V_{j-1}, so s_full covers both and
-      // O_t may be rescaled now.
-      if (j > 0 && __any_sync(0xffffffffu, raise)) {
-#pragma unroll 1
-        for (int q = 0; q < DV / 64; ++q) {
-          uint32_t ov[32];
-          tmem_ld32(tO + 32 * q, ov);
-          tmem_ld_wait();
-          reg_fence(ov);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-          tmem_st32(tO + 32 * q, ov);
+      // The maximum is raised in few blocks. So the exponentials above have gone
+      // ahead with the old one, and the two warps meet afterwards, when neither
+      // has to wait long; if a row of either half asks for a raise, O_t is
+      // rescaled and the pass is made again.
+      if (!named_bar_and(pair_bar, 64, keep)) {
+        if (!named_bar_and(pair_bar, 64, ready)) {
+          ok = false;
+          break;
         }
-      }
-      const float mu = (m == -INFINITY) ? 0.f : m;
-      const uint64_t sl2x2 = f2(sl2, sl2);
-      const uint64_t negmu2 = f2(-mu, -mu);
-      uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
-      // S is read again 32 columns at a time; P of columns 0-31 goes to
-      // columns 0-15, P of 32-63 to 16-31, each after the S values under it
-      // have been read.
+        const float m_blk = fmaxf(pm, slot[(c ^ 1) * 128 + r]) * sl2;
+        float alpha = 1.f;
+        if (m_blk > m + 8.0f) {
+          alpha = ex2(m - m_blk);  // 0 when m was -inf
+          m = m_blk;
+        }
+        l *= alpha;
+        // S_t(j) was issued after P_t(j-1) V_{j-1}, so s_full covers both and
+        // O_t may be rescaled now.
+        if (j > 0) {
+#pragma unroll 1
+          for (int q = 0; q < DV / 64; ++q) {
+            uint32_t ov[32];
+            tmem_ld32(tO + 32 * q, ov);
+            tmem_ld_wait();
+            reg_fence(ov);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t sv[32];
-        tmem_ld32(tS + 32 * q, sv);
-        tmem_ld_wait();
-        reg_fence(sv);
-        uint32_t pw[16];
-        if (masked)
-          fwd_exp32<BF16, true>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw);
-        else
-          fwd_exp32<BF16, false>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw);
-        tmem_st16(tS + 16 * q, pw);
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(tO + 32 * q, ov);
+          }
+        }
+        pass(std::true_type{});
       }
-      {
-        const uint64_t acc = add2(acc0, acc1);
-        float a0, a1;
-        f2_split(acc, a0, a1);
-        l += a0 + a1;
-      }
+      l += add;
+      tmem_st16(tS, pw[0]);  // over this half's own columns of S
+      tmem_st16(tS + 16, pw[1]);
       if (t == 0 && a.k_lens != nullptr && j == n - 1 && (j + 1) * 128 > sk) {
         // V rows past this sequence's last key (whatever a cache holds there)
         // become zeros before P V reads them: their P is 0, but 0 x inf is
