@@ -18,7 +18,9 @@
 //  2. fa_diff_bwd_main: one CTA per (batch, key head, 128-key block); walks the
 //     query blocks of every query head that shares the key head, so dK and dV
 //     of shared heads are summed in the CTA's fp32 accumulators, in a fixed
-//     order.
+//     order. Where the longest such list would outlast the rest of the grid
+//     (few key heads, many query heads, a causal mask), the lists are cut into
+//     parts, a CTA each, whose fp32 dK and dV fa_diff_dkv adds in order.
 //  3. fa_diff_dq: dq_c = scale * accumulator, rounded to the input dtype.
 //  4. fa_diff_lam_few, or fa_diff_lam_part and fa_diff_lam_sum: dlambda, summed over the axes lambda
 //     is broadcast over in a fixed order.
@@ -69,9 +71,11 @@ struct DiffBwdArgs {
   float* dq_acc;   // fp32 [2][B*H][Sq_pad][64]
   float* vec;      // fp32 [B*H][Sq_pad / 64][5][64]: -lse2_1, -lse2_2, -lambda, -Delta_1, -Delta_2
   float* drow;     // fp32 [B][H][Sq]: -Delta_2
+  float* dkv_part;  // parts > 1: fp32 [parts][B*Hk][Sk_pad][128 + DV]: a part's dK_1, dK_2, dV; else null
   float* dq_part;  // deterministic mode: fp32 [B*H][nqb][nkb][2][128][64] slots; else null
   int B, H, Hk, Sq, Sk, Sq_pad;
   int nqb, nkb;    // ceil(Sq / 128), ceil(Sk / 128)
+  int parts;       // CTAs that share a key block's (head, query block) list
   int d, dv_cols;  // head_dim of q and k; columns of v
   float scale, scale_log2;
   int causal;
@@ -251,6 +255,44 @@ __global__ void __launch_bounds__(256) fa_diff_dq(const DiffBwdArgs a) {
                               h * a.dq_s[c][2] + part * 8) = out;
 }
 
+// ------------------------------------------------------------ dk, dv join
+// dk_c and dv of key blocks whose query blocks were cut into parts: the parts'
+// sums are added in order. 8 columns per thread of a row of dK_1 | dK_2 | dV.
+template <int DV, bool BF16>
+__global__ void __launch_bounds__(256) fa_diff_dkv(const DiffBwdArgs a) {
+  constexpr int G = (128 + DV) / 8;
+  const int64_t gid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t row = gid / G;  // (b, hk, key)
+  const int part = static_cast<int>(gid % G);
+  const int64_t bhs = static_cast<int64_t>(a.B) * a.Hk;
+  if (row >= bhs * a.Sk) return;
+  const int key = static_cast<int>(row % a.Sk);
+  const int bh = static_cast<int>(row / a.Sk);
+  const int hk = bh % a.Hk, b = bh / a.Hk;
+  const bool is_k = part < 16;
+  const int c = part >> 3;  // map, for dK
+  const int col = is_k ? (part & 7) * 8 : (part - 16) * 8;
+  if (col >= (is_k ? a.d : a.dv_cols)) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int64_t step = bhs * a.nkb * 128 * (128 + DV);
+  const float* src = a.dkv_part + (static_cast<int64_t>(bh) * a.nkb * 128 + key) * (128 + DV) + part * 8;
+  for (int p = 0; p < a.parts; ++p) {
+    const float4 x = reinterpret_cast<const float4*>(src + p * step)[0];
+    const float4 y = reinterpret_cast<const float4*>(src + p * step)[1];
+    acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+    acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+  }
+  const float s = is_k ? a.scale : 1.f;
+  uint4 out;
+  out.x = sm100::pack2<BF16>(acc[0] * s, acc[1] * s);
+  out.y = sm100::pack2<BF16>(acc[2] * s, acc[3] * s);
+  out.z = sm100::pack2<BF16>(acc[4] * s, acc[5] * s);
+  out.w = sm100::pack2<BF16>(acc[6] * s, acc[7] * s);
+  uint16_t* dst = is_k ? reinterpret_cast<uint16_t*>(a.dk[c]) + b * a.dk_s[c][0] + key * a.dk_s[c][1] + hk * a.dk_s[c][2]
+                       : reinterpret_cast<uint16_t*>(a.dv) + b * a.dv_s[0] + key * a.dv_s[1] + hk * a.dv_s[2];
+  if (checked(b < a.B && key < a.Sk, 505)) *reinterpret_cast<uint4*>(dst + col) = out;
+}
+
 // ----------------------------------------------------------- dlambda sums
 // dlambda has extents ext[] (each 1 or the full axis; order batch, row, head)
 // and is dense. Element x sums drow over the axes with extent 1: `count` terms,
@@ -414,8 +456,10 @@ __global__ void __launch_bounds__(448, 1)
   // the first key blocks (the most query blocks) first; without one
   // head-major.
   const int hb_count = a.Hk * a.B;
-  const int kvb = a.causal ? static_cast<int>(blockIdx.x) / hb_count : static_cast<int>(blockIdx.x) % a.nkb;
-  const int hb = a.causal ? static_cast<int>(blockIdx.x) % hb_count : static_cast<int>(blockIdx.x) / a.nkb;
+  const int part = static_cast<int>(blockIdx.x) % a.parts;
+  const int cta = static_cast<int>(blockIdx.x) / a.parts;
+  const int kvb = a.causal ? cta / hb_count : cta % a.nkb;
+  const int hb = a.causal ? cta % hb_count : cta / a.nkb;
   const int hk = hb % a.Hk;
   const int b = hb / a.Hk;
   const int group = a.H / a.Hk;
@@ -423,10 +467,13 @@ __global__ void __launch_bounds__(448, 1)
   const int off = a.Sk - a.Sq;
   const int i_start = bwd_first_qblock(kvb, a.Sq, a.Sk, a.causal);
   const int nb = max(0, a.nqb - i_start);  // query blocks of one head
-  const int n = 2 * nb * group;            // chunks
+  // This CTA's part of the list of (head, query block) pairs; two chunks each.
+  const int64_t listed = static_cast<int64_t>(nb) * group;
+  const int blk0 = static_cast<int>(listed * part / a.parts);
+  const int n = 2 * (static_cast<int>(listed * (part + 1) / a.parts) - blk0);
   // Chunk i: its head's (b, h) row base and its first query row.
-  auto chunk_bh = [&](int i) { return b * a.H + hk * group + (i >> 1) / nb; };
-  auto chunk_row = [&](int i) { return (i_start + (i >> 1) % nb) * 128 + (i & 1) * 64; };
+  auto chunk_bh = [&](int i) { return b * a.H + hk * group + (blk0 + (i >> 1)) / nb; };
+  auto chunk_row = [&](int i) { return (i_start + (blk0 + (i >> 1)) % nb) * 128 + (i & 1) * 64; };
   const int64_t acc_rows = static_cast<int64_t>(a.B) * a.H * a.Sq_pad;  // of one map's dQ accumulator
 
   if (threadIdx.x == 0) {
@@ -800,7 +847,8 @@ __global__ void __launch_bounds__(448, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_ready);
     }
-    // Epilogue: warpgroup 0 writes dK_c = scale * accumulator, warpgroup 1 dV.
+    // Epilogue: warpgroup 0 writes dK_c = scale * accumulator, warpgroup 1 dV
+    // (or, of several parts, the fp32 accumulators: fa_diff_dkv joins them).
     if (ok && !*abort_flag) {
       const bool have = n > 0;
       if (!have || __all_sync(0xffffffffu, wait_bar(mma_done, 0, abort_flag, kRoleSoftmax, n))) {
@@ -824,7 +872,19 @@ __global__ void __launch_bounds__(448, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0u;
           }
-          if (key < a.Sk && checked(b < a.B && hk < a.Hk, 512)) {
+          if (a.dkv_part != nullptr) {
+            // Keys past Sk have rows here too (Sk_pad).
+            float4* f = reinterpret_cast<float4*>(
+                a.dkv_part +
+                (((static_cast<int64_t>(part) * a.B + b) * a.Hk + hk) * a.nkb * 128 + key) * (128 + DV) +
+                (g == 0 ? 0 : 128) + 32 * x);
+            if (checked(part < a.parts && key < a.nkb * 128, 515)) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                f[u] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                                   __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+            }
+          } else if (key < a.Sk && checked(b < a.B && hk < a.Hk, 512)) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t w[4];

@@ -169,7 +169,7 @@ def lib():
         L.fa_diff_fwd_workspace_size.restype = sz
         L.fa_diff_bwd.argtypes = [ctypes.POINTER(DiffBwdParams), vp]
         L.fa_diff_bwd.restype = i
-        L.fa_diff_bwd_workspace_size.argtypes = [i, i, i, i, i]
+        L.fa_diff_bwd_workspace_size.argtypes = [i, i, i, i, i, i, i, i, i]
         L.fa_diff_bwd_workspace_size.restype = sz
         L.fa_rotary.argtypes = [ctypes.POINTER(RotaryParams), vp]
         L.fa_rotary.restype = i
@@ -253,8 +253,8 @@ def fa_diff_bwd(params: DiffBwdParams, stream=0) -> int:
     return lib().fa_diff_bwd(ctypes.byref(params), stream)
 
 
-def fa_diff_bwd_workspace_size(B, H, Sq, Sk, deterministic) -> int:
-    return lib().fa_diff_bwd_workspace_size(B, H, Sq, Sk, deterministic)
+def fa_diff_bwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal, deterministic) -> int:
+    return lib().fa_diff_bwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal, deterministic)
 
 
 def fa_rotary(params: RotaryParams, stream=0) -> int:
@@ -689,12 +689,14 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=Non
     dq, dk, dv, dlam = grads
     if not dlam.is_contiguous():
         raise ValueError("dlam must be contiguous")
+    causal = 1 if causal else 0
     if workspace is None:
-        workspace = torch.empty(fa_diff_bwd_workspace_size(B, H, Sq, Sk, det), dtype=torch.uint8, device=dev)
+        n = fa_diff_bwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal, det)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     p = _DIFF_BWD.pack(*_pair("q", q), *_pair("k", k), *_flat("v", v), *_flat("o", o), *_flat("o2", o2),
                        *_flat("do", do), lse.data_ptr(), *lp, *_pair("dq", dq), *_pair("dk", dk), *_flat("dv", dv),
                        dlam.data_ptr(), B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale),
-                       1 if causal else 0, dt, *_ws(workspace, dev), det)
+                       causal, dt, *_ws(workspace, dev), det)
     st = _packed("fa_diff_bwd")(p, _raw_stream(dev.index))
     if st != FA_OK:
         raise FaError(st, "fa_diff_bwd")

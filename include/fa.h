@@ -373,11 +373,13 @@ size_t fa_diff_fwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, i
    (k_lens NULL). */
 int fa_diff_bwd(const fa_diff_bwd_params* p, fa_stream_t stream);
 
-/* Workspace bytes of fa_diff_bwd: both maps' fp32 dq accumulators
-   [2, B, H, Sq_pad, 64] (deterministic: one [2][128][64] slot per query block
-   and key block instead), five row terms per padded row, one per row and 4 KB.
-   0 for arguments that fa_diff_bwd refuses. */
-size_t fa_diff_bwd_workspace_size(int B, int H, int Sq, int Sk, int deterministic);
+/* Workspace bytes of fa_diff_bwd on the current device: both maps' fp32 dq
+   accumulators [2, B, H, Sq_pad, 64] (deterministic: one [2][128][64] slot per
+   query block and key block instead), five row terms per padded row, one per
+   row and 4 KB; where the work of a key block is cut into parts (few key heads
+   shared by many query heads), fp32 dk and dv of every part. Host only. 0 for
+   arguments that fa_diff_bwd refuses. */
+size_t fa_diff_bwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, int causal, int deterministic);
 
 /* ------------------------------------------- rotary positions, several axes
    Turns the first 2R columns of every head of q and k, as R pairs: columns

@@ -137,14 +137,15 @@ def test_rotary_refuses(fa_lib, kw, code):
 
 
 def test_workspace_sizes(fa_lib):
-    # both maps' accumulators [2, B*H*Sq_pad, 64], five row terms, one per row (rounded up), 4 KB
+    # both maps' accumulators [2, B*H*Sq_pad, 64], five row terms, one per row (rounded up), 4 KB (one part:
+    # three query blocks a head are too few to cut)
     rows = 2 * 3 * 256
     want = (rows * (128 + 5) * 4 + 2 * 3 * 200 * 4 + 255) // 256 * 256 + 4096
-    assert fa.fa_diff_bwd_workspace_size(2, 3, 200, 300, 0) == want
+    assert fa.fa_diff_bwd_workspace_size(2, 3, 3, 200, 300, 64, 128, 0, 0) == want
     det = (2 * 3 * 2 * 3 * 2 * 128 * 64 * 4 + rows * 5 * 4 + 2 * 3 * 200 * 4 + 255) // 256 * 256 + 4096
-    assert fa.fa_diff_bwd_workspace_size(2, 3, 200, 300, 1) == det
-    assert fa.fa_diff_bwd_workspace_size(2, 3, 200, 300, 2) == 0
-    assert fa.fa_diff_bwd_workspace_size(2, 3, 0, 300, 0) == 0
+    assert fa.fa_diff_bwd_workspace_size(2, 3, 3, 200, 300, 64, 128, 0, 1) == det
+    assert fa.fa_diff_bwd_workspace_size(2, 3, 3, 200, 300, 64, 128, 0, 2) == 0
+    assert fa.fa_diff_bwd_workspace_size(2, 3, 3, 0, 300, 64, 128, 0, 0) == 0
     assert fa.fa_diff_fwd_workspace_size(1, 8, 8, 4096, 4096, 64, 128, 1) == 0
     assert fa.fa_diff_fwd_workspace_size(1, 8, 3, 1, 4096, 64, 128, 1) == 0  # refused: 3 does not divide 8
 

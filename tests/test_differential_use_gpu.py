@@ -73,6 +73,20 @@ def test_graph_of_the_forward(fa_lib, Sq):
     status_clear()
 
 
+@pytest.mark.parametrize("c", [(1, 1000, 1000, 8, 1, 64, 128, torch.bfloat16, True),
+                               (1, 900, 130, 6, 2, 40, 64, torch.float16, False),
+                               (2, 700, 1100, 4, 1, 64, 72, torch.float16, True)], ids=["8-1", "6-2", "4-1"])
+def test_backward_in_parts(fa_lib, c):
+    """Many query heads on few key heads: the key blocks' lists are cut into parts and joined."""
+    B, Sq, Sk, H, Hk, D, Dv, dtype, causal = c
+    whole = 4 * (B * H * -(-Sq // 128) * 128 * (2 * 64 + 5) + B * H * Sq) + 256 + 4096  # the workspace of one part
+    assert fa.fa_diff_bwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, int(causal), 0) > whole
+    x = case(B, Sq, Sk, H, Hk, D, Dv, dtype, 43, "head", torch.float32)
+    full_check(x, causal)
+    one, two = (full_check(x, causal, deterministic=True) for _ in range(2))
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
 def test_graph_of_a_training_pass(fa_lib):
     B, Sq, Sk, H, Hk, D, Dv = 1, 200, 260, 4, 2, 64, 128
     sets = [[x.cuda() for x in case(B, Sq, Sk, H, Hk, D, Dv, torch.float16, 70 + i, "token")] for i in range(2)]
@@ -168,7 +182,7 @@ def test_guard_bands(fa_lib, c):
     fws_big, fws = flat(n, torch.uint8)
     o, lse, o2 = fa.diff_forward(q, k, v, w, causal=causal, out=out("o", o_like), out2=out("o2", o_like),
                                  lse=lse.view(2, B, H, Sq), workspace=fws if n else None)
-    n = fa.fa_diff_bwd_workspace_size(B, H, Sq, Sk, 0)
+    n = fa.fa_diff_bwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, int(causal), 0)
     ws_big, ws = flat(n, torch.uint8)
     dl_big, dl = flat(max(1, w.numel()), w.dtype)
     fa.diff_backward(q, k, v, w, o.contiguous(), o2.contiguous(), lse, do, causal=causal, dq=out("dq", q),
