@@ -173,7 +173,7 @@ int launch_diff_rows(const fa_diff_fwd_params* p, const RowsPlan& plan, cudaStre
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(p->workspace) + plan.off_o);
   }
   const unsigned grid = unsigned(int64_t(p->B) * p->Hk * a.n_mt * a.n_split);
-  kern<<<grid, 128, L::SMEM_ALLOC, stream>>>(mk[0], mk[1], mv, a);
+  kern<<<grid, 256, L::SMEM_ALLOC, stream>>>(mk[0], mk[1], mv, a);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (plan.n_split > 1) {
     // Launched while the runs still work (programmatic dependent launch): its

@@ -6,13 +6,15 @@
 // kernel is built around that stream: the keys are cut into `n_split` runs,
 // one CTA per (batch, key head, run, 16 rows). All rows that share a key head
 // form one 16-row operand of m16n8k16 products, so shared heads read their
-// keys once. Each of the four warps streams its own 16-key tiles through a ring of
-// NS stages filled by TMA (its lane 0 issues the loads and the warp waits on
-// the stage's mbarrier: no producer warp, no block-wide barrier in the loop)
-// and keeps its own running maxima, sums and unnormalised O_1, O_2. The four
-// warps' results join in shared memory, the runs' in a second small kernel
-// (fa_diff_rows_join), both by the online softmax's rescaling. Two CTAs share
-// an SM, so one's start and end overlap the other's stream.
+// keys once. A CTA has four streams of two warps, one warp per map. Each stream
+// takes every fourth 16-key tile through a ring of NS stages filled by TMA (a
+// lane of its first warp issues the loads; both warps wait on the stage's
+// mbarrier and hand it back through another: no producer warp, no block-wide
+// barrier in the loop), and each warp keeps its map's running maximum, sum and
+// unnormalised O. The streams' results join in shared memory, the runs' in a
+// second small kernel (fa_diff_rows_join), both by the online softmax's
+// rescaling. Two CTAs share an SM, so one's start and end overlap the other's
+// stream. (One warp for both maps: 4 warps of 253 registers, XX us slower.)
 //
 // P is split into two 16-bit terms, p = hi + lo, and multiplied with V twice:
 // the tensor cores have time to spare here, and O keeps the fp32 accuracy of P.
@@ -56,8 +58,8 @@ struct DiffRowsLayout {
   static constexpr int OROW = DV + 4;
   static constexpr int JOIN = 4 * 2 * 16 * OROW * 4;
   static constexpr int OFF_ML = RING > JOIN ? RING : JOIN;  // [warp][map][16] (m, l)
-  static constexpr int OFF_BAR = OFF_ML + 4 * 2 * 16 * 8;
-  static constexpr int OFF_MISC = OFF_BAR + 4 * NS * 8;
+  static constexpr int OFF_BAR = OFF_ML + 4 * 2 * 16 * 8;  // full, empty [stream][stage]
+  static constexpr int OFF_MISC = OFF_BAR + 2 * 4 * NS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM_ALLOC = BYTES + 1024;
 };
@@ -113,7 +115,7 @@ __device__ __forceinline__ void diff_row_out(const Args& a, int b, int h, int ro
 }
 
 template <int DV, bool BF16>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(256, 2)
     fa_diff_rows_kernel(const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmK2,
                         const __grid_constant__ CUtensorMap tmV, const DiffRowsArgs a) {
   using L = DiffRowsLayout<DV>;
@@ -124,32 +126,40 @@ __global__ void __launch_bounds__(128, 2)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   float2* ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stream = threadIdx.x >> 6, c = (threadIdx.x >> 5) & 1;  // c: the warp's map
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;  // fragment row group and column pair
 
+  // Heads before runs: the CTAs that run together read neighbouring heads of the
+  // same keys, which lie side by side in memory.
   const int mt = static_cast<int>(blockIdx.x) % a.n_mt;
-  const int split = static_cast<int>(blockIdx.x) / a.n_mt % a.n_split;
-  const int bk = static_cast<int>(blockIdx.x) / a.n_mt / a.n_split;
-  const int hk = bk % a.Hk, b = bk / a.Hk;
+  const int hk = static_cast<int>(blockIdx.x) / a.n_mt % a.Hk;
+  const int split = static_cast<int>(blockIdx.x) / a.n_mt / a.Hk % a.n_split;
+  const int b = static_cast<int>(blockIdx.x) / a.n_mt / a.Hk / a.n_split;
+  const int bk = b * a.Hk + hk;
   const int group = a.H / a.Hk;
   const int len = diff_keys(a.k_lens, b, a.Sk);
   const int lo = split * a.chunk, hi = min(len, lo + a.chunk);
   const int tiles = hi > lo ? (hi - lo + KT - 1) / KT : 0;
-  const int mine = tiles > warp ? (tiles - warp + 3) / 4 : 0;  // this warp's tiles: warp, warp + 4, ...
+  const int mine = tiles > stream ? (tiles - stream + 3) / 4 : 0;  // this stream's tiles: stream, stream + 4, ...
   checked(b < a.B && mt * 16 < a.R, 601);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * NS; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 4 * NS; ++i) {
+      mbar_init(&bars[i], 1);
+      mbar_init(&bars[4 * NS + i], 2);  // one arrival per map's warp
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  uint64_t* full = bars + warp * NS;
-  uint8_t* ring = smem + warp * NS * L::TILE;
-  auto issue = [&](int i) {  // lane 0: tile i of this warp into its stage
-    const int st = i % NS, key = lo + (warp + 4 * i) * KT;
+  uint64_t* full = bars + stream * NS;
+  uint64_t* empty = bars + (4 + stream) * NS;
+  uint8_t* ring = smem + stream * NS * L::TILE;
+  auto issue = [&](int i) {  // one lane: tile i of this stream into its stage
+    const int st = i % NS, key = lo + (stream + 4 * i) * KT;
     uint8_t* dst = ring + st * L::TILE;
     checked(key < a.Sk, 602);
     mbar_arrive_expect_tx(&full[st], L::TILE);
@@ -158,41 +168,35 @@ __global__ void __launch_bounds__(128, 2)
 #pragma unroll
     for (int vb = 0; vb < L::VB; ++vb) tma_load_4d(dst + (2 + vb) * KT * 128, &tmV, &full[st], vb * 64, key, hk, b);
   };
-  if (lane == 0)
-    for (int i = 0; i < min(NS, mine); ++i) issue(i);
+  const bool loads = c == 0 && lane == 0;
+  int issued = 0;
+  if (loads)
+    for (; issued < min(NS, mine); ++issued) issue(issued);
 
   // Row r of the tile: query row i = r % Sq of head hk * group + r / Sq.
   int lim[2];  // last key that rows g and g + 8 see
-  uint32_t qf[2][4][4];
+  uint32_t qf[4][4];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = mt * 16 + g + 8 * e;
     const int i = r % a.Sq, h = hk * group + r / a.Sq;
     lim[e] = a.causal && r < a.R ? i + len - a.Sq : len - 1;  // rows past R are not written
+    const uint16_t* p = (c ? a.q[1] : a.q[0]) + b * a.q_s[c][0] + i * a.q_s[c][1] + h * a.q_s[c][2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint16_t* p = a.q[c] + b * a.q_s[c][0] + i * a.q_s[c][1] + h * a.q_s[c][2];
+    for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int col = ks * 16 + x * 8 + 2 * tq;
-          qf[c][ks][2 * x + e] = r < a.R && col < a.d ? *reinterpret_cast<const uint32_t*>(p + col) : 0u;
-        }
-    }
+      for (int x = 0; x < 2; ++x) {
+        const int col = ks * 16 + x * 8 + 2 * tq;
+        qf[ks][2 * x + e] = r < a.R && col < a.d ? *reinterpret_cast<const uint32_t*>(p + col) : 0u;
+      }
   }
   const int min_lim = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
-  float m[2][2], l[2][2];  // [map][row g / g + 8]
-  float acc[2][NT][4];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8
+  float acc[NT][4];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m[c][e] = -INFINITY, l[c][e] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.f;
-  }
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
   const float sl2 = a.scale_log2;
   // ldmatrix row addresses: K, matrices = 16-byte chunks 0-3 of 8 keys; V,
   // matrices = (keys 0-7, 8-15) x (chunk, chunk + 1), transposed.
@@ -200,114 +204,114 @@ __global__ void __launch_bounds__(128, 2)
   const int vr = (km & 1) * 8 + kr, vm = km >> 1;
 
   bool ok = true;
-  int i = 0;
-  for (; i < mine; ++i) {
-    const int st = i % NS, key0 = lo + (warp + 4 * i) * KT;
-    if (!(ok = __all_sync(0xffffffffu, wait_bar(&full[st], (i / NS) & 1, abort_flag, kRoleSoftmax, i)))) break;
+  for (int i = 0; i < mine; ++i) {
+    const int st = i % NS, key0 = lo + (stream + 4 * i) * KT;
+    if (!(ok = __all_sync(0xffffffffu, wait_bar_c(&full[st], (i / NS) & 1, abort_flag, kRoleSoftmax, i)))) break;
     uint8_t* tile = ring + st * L::TILE;
-    const uint32_t sk = smem_u32(tile), sv = sk + 2 * KT * 128;
-    if (key0 + KT > len) {  // rows past the end count nothing, whatever they hold
+    const uint32_t sk = smem_u32(tile) + c * KT * 128, sv = smem_u32(tile) + 2 * KT * 128;
+    if (key0 + KT > len) {
+      // Rows past the end count nothing, whatever they hold. (Both warps of the
+      // stream write the same zeros, each for itself; it is the last tile.)
       for (int x = lane; x < L::VB * KT * 8; x += 32)
         if (key0 + ((x >> 3) & (KT - 1)) >= len) st_shared_v4(sv + x * 16, 0, 0, 0, 0);
       __syncwarp();
     }
-    uint32_t ph[2][4], pl[2][4];
+    float s[2][4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float s[2][4];
+    for (int n = 0; n < 2; ++n) {
+      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      const int row = n * 8 + kr;
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        const int row = n * 8 + kr;
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t f[4];
+        ldsm_x4(f, sk + row * 128 + (((hf * 4 + km) ^ (row & 7)) << 4));
+        mma16816<BF16>(s[n], qf[2 * hf], f[0], f[1]);
+        mma16816<BF16>(s[n], qf[2 * hf + 1], f[2], f[3]);
+      }
+    }
+    const bool masked = key0 + KT - 1 > min_lim;
+    uint32_t ph[4], pl[4];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t f[4];
-          ldsm_x4(f, sk + c * KT * 128 + row * 128 + (((hf * 4 + km) ^ (row & 7)) << 4));
-          mma16816<BF16>(s[n], qf[c][2 * hf], f[0], f[1]);
-          mma16816<BF16>(s[n], qf[c][2 * hf + 1], f[2], f[3]);
+    for (int e = 0; e < 2; ++e) {
+      if (masked) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (key0 + n * 8 + 2 * tq + x > lim[e]) s[n][2 * e + x] = -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      mx *= sl2;
+      // As in the other forwards, a stale maximum is kept within 2^8.
+      const bool raise = mx > m[e] + 8.f;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float alpha = raise ? ex2(m[e] - mx) : 1.f;
+        if (raise) m[e] = mx;
+        l[e] *= alpha;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[n][2 * e] *= alpha;
+          acc[n][2 * e + 1] *= alpha;
         }
       }
-      const bool masked = key0 + KT - 1 > min_lim;
+      const float mu = m[e] == -INFINITY ? 0.f : m[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (masked) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (key0 + n * 8 + 2 * tq + x > lim[e]) s[n][2 * e + x] = -INFINITY;
-        }
-        float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx *= sl2;
-        // As in the other forwards, a stale maximum is kept within 2^8.
-        const bool raise = mx > m[c][e] + 8.f;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float alpha = raise ? ex2(m[c][e] - mx) : 1.f;
-          if (raise) m[c][e] = mx;
-          l[c][e] *= alpha;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[c][n][2 * e] *= alpha;
-            acc[c][n][2 * e + 1] *= alpha;
-          }
-        }
-        const float mu = m[c][e] == -INFINITY ? 0.f : m[c][e];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2(fmaf(s[n][2 * e], sl2, -mu)), p1 = ex2(fmaf(s[n][2 * e + 1], sl2, -mu));
-          l[c][e] += p0 + p1;
-          const uint32_t w = pack2<BF16>(p0, p1);
-          const float2 r = unpack2<BF16>(w);
-          ph[c][2 * n + e] = w;
-          pl[c][2 * n + e] = pack2<BF16>(p0 - r.x, p1 - r.y);
-        }
+      for (int n = 0; n < 2; ++n) {
+        const float p0 = ex2(fmaf(s[n][2 * e], sl2, -mu)), p1 = ex2(fmaf(s[n][2 * e + 1], sl2, -mu));
+        l[e] += p0 + p1;
+        const uint32_t w = pack2<BF16>(p0, p1);
+        const float2 r = unpack2<BF16>(w);
+        ph[2 * n + e] = w;
+        pl[2 * n + e] = pack2<BF16>(p0 - r.x, p1 - r.y);
       }
     }
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
       uint32_t f[4];
       ldsm_x4_t(f, sv + (n >> 3) * KT * 128 + vr * 128 + ((((n & 7) + vm) ^ (vr & 7)) << 4));
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        mma16816<BF16>(acc[c][n], ph[c], f[0], f[1]);
-        mma16816<BF16>(acc[c][n + 1], ph[c], f[2], f[3]);
-        mma16816<BF16>(acc[c][n], pl[c], f[0], f[1]);
-        mma16816<BF16>(acc[c][n + 1], pl[c], f[2], f[3]);
-      }
+      mma16816<BF16>(acc[n], ph, f[0], f[1]);
+      mma16816<BF16>(acc[n + 1], ph, f[2], f[3]);
+      mma16816<BF16>(acc[n], pl, f[0], f[1]);
+      mma16816<BF16>(acc[n + 1], pl, f[2], f[3]);
     }
     __syncwarp();
-    if (lane == 0 && i + NS < mine) issue(i + NS);
+    if (lane == 0) mbar_arrive(&empty[st]);
+    if (loads && i + NS < mine) {
+      // The other map's warp is at most a tile behind in the same stage.
+      if (!wait_bar_c(&empty[st], (i / NS) & 1, abort_flag, kRoleLoader, i)) break;  // the abort flag is up
+      issue(i + NS);
+      ++issued;
+    }
   }
-  if (!ok && lane == 0)  // let the copies already issued land before the CTA exits
-    for (int x = i; x < min(mine, i + NS); ++x) drain_wait(&full[x % NS], (x / NS) & 1);
+  if (loads && *abort_flag)  // let the copies already issued land before the CTA exits
+    for (int x = max(0, issued - NS); x < issued; ++x) drain_wait(&full[x % NS], (x / NS) & 1);
+  __syncwarp();
   __syncthreads();  // every warp has read its last tile: the ring becomes the join's buffer
   if (*abort_flag) return;
 
   float* jo = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+  for (int e = 0; e < 2; ++e) {
+    float s = l[e];
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (tq == 0) ml[(stream * 2 + c) * 16 + g + 8 * e] = make_float2(m[e], s);
+    float* row = jo + ((stream * 2 + c) * 16 + g + 8 * e) * L::OROW;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float s = l[c][e];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (tq == 0) ml[(warp * 2 + c) * 16 + g + 8 * e] = make_float2(m[c][e], s);
-      float* row = jo + ((warp * 2 + c) * 16 + g + 8 * e) * L::OROW;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(row + n * 8 + 2 * tq) = make_float2(acc[c][n][2 * e], acc[c][n][2 * e + 1]);
-    }
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float2*>(row + n * 8 + 2 * tq) = make_float2(acc[n][2 * e], acc[n][2 * e + 1]);
+  }
   __syncthreads();
   // Rows of the tile x groups of 4 columns over the block's threads.
-  for (int x = threadIdx.x; x < 16 * (DV / 4); x += 128) {
+  for (int x = threadIdx.x; x < 16 * (DV / 4); x += 256) {
     const int tr = x / (DV / 4), col = x % (DV / 4) * 4;
     const int r = mt * 16 + tr;
     if (r >= a.R) break;
     float o[2][4], mm[2], ll[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < 2; ++c) {  // both maps
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[(w * 2 + c) * 16 + tr].x);
