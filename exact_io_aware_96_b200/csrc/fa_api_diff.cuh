@@ -103,31 +103,29 @@ int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// The few-row form (fa_diff_rows.cuh): whether a call takes it, and its key
-// runs. A CTA streams its run at the SM's share of the memory bandwidth, two
-// CTAs to an SM; runs are cut so that the grid fills the SMs about twice over,
-// at no less than 128 keys (two tiles per warp).
+// The few-row form (fa_diff_rows.cuh): whether a call takes it, and its teams.
+// Two CTAs run on an SM. Where a team of one CTA per (key head, row tile) is
+// small, as many teams as fit at once share the keys evenly; large teams get a
+// few waves, which even out by themselves. Many batch entries, or caches of two
+// units per stream at most, go direct: no second kernel.
 struct RowsPlan {
-  int chunk = 0, n_split = 0;  // n_split 0: the tiled kernel
+  bool rows = false;  // false: the tiled kernel
+  int teams = 0;      // 0: direct
   uint64_t off_o = 0, bytes = 0;
 };
 RowsPlan rows_plan(int B, int H, int Hk, int Sq, int Sk, int Dv) {
   RowsPlan p;
   const int64_t R = int64_t(H / Hk) * Sq;
   if (Sq > 16 || R > 64) return p;
-  const int sms = std::max(1, sm_count());
-  const int64_t items = int64_t(B) * Hk * ((R + 15) / 16);
-  const int64_t want = (4 * sms + items - 1) / items;  // runs per item
-  int64_t chunk = (Sk + want - 1) / want;
-  chunk = std::max<int64_t>(128, (chunk + 63) / 64 * 64);
-  p.chunk = int(std::min<int64_t>(chunk, (int64_t(Sk) + 63) / 64 * 64));
-  p.n_split = int((int64_t(Sk) + p.chunk - 1) / p.chunk);
-  if (items * p.n_split > (int64_t(1) << 31) - 1) return RowsPlan();
-  if (p.n_split > 1) {
-    const uint64_t slots = uint64_t(B) * Hk * R * p.n_split * 2;
-    p.off_o = round256(slots * sizeof(float2));
-    p.bytes = p.off_o + slots * (Dv <= 64 ? 64 : 128) * 4;
-  }
+  const int64_t slots = 2 * int64_t(std::max(1, sm_count())), team = int64_t(Hk) * ((R + 15) / 16);
+  if (team * B > (int64_t(1) << 31) - 1) return p;
+  p.rows = true;
+  if (Sk <= 256 || team * B >= 4 * slots) return p;
+  const int64_t teams = team * 4 <= slots ? slots / team : (4 * slots + team - 1) / team;
+  p.teams = int(std::min<int64_t>(teams, (int64_t(B) * ((int64_t(Sk) + 63) / 64) + 1) / 2));
+  const uint64_t parts = uint64_t(B + p.teams) * Hk * R * 2;
+  p.off_o = round256(parts * sizeof(float2));
+  p.bytes = p.off_o + parts * (Dv <= 64 ? 64 : 128) * 4;
   return p;
 }
 
@@ -165,18 +163,17 @@ int launch_diff_rows(const fa_diff_fwd_params* p, const RowsPlan& plan, cudaStre
   a.causal = p->causal;
   a.R = p->H / p->Hk * p->Sq;
   a.n_mt = (a.R + 15) / 16;
-  a.chunk = plan.chunk;
-  a.n_split = plan.n_split;
-  if (plan.n_split > 1) {
+  a.teams = plan.teams;
+  if (plan.teams > 0) {
     if (p->workspace == nullptr || p->workspace_bytes < plan.bytes) return FA_ERR_WORKSPACE;
     a.part_ml = static_cast<float2*>(p->workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(p->workspace) + plan.off_o);
   }
-  const unsigned grid = unsigned(int64_t(p->B) * p->Hk * a.n_mt * a.n_split);
+  const unsigned grid = unsigned(int64_t(plan.teams > 0 ? plan.teams : p->B) * p->Hk * a.n_mt);
   kern<<<grid, 256, L::SMEM_ALLOC, stream>>>(mk[0], mk[1], mv, a);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (plan.n_split > 1) {
-    // Launched while the runs still work (programmatic dependent launch): its
+  if (plan.teams > 0) {
+    // Launched while the pieces are worked on (programmatic dependent launch): its
     // blocks wait on the device for the whole first grid.
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -421,7 +418,7 @@ int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream) {
   if (p->workspace != nullptr && (reinterpret_cast<uintptr_t>(p->workspace) & 255u)) return FA_ERR_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RowsPlan plan = rows_plan(p->B, p->H, p->Hk, p->Sq, p->Sk, p->Dv);
-  if (plan.n_split > 0) {
+  if (plan.rows) {
     if (p->Dv <= 64)
       return p->dtype == FA_BF16 ? launch_diff_rows<64, true>(p, plan, s) : launch_diff_rows<64, false>(p, plan, s);
     return p->dtype == FA_BF16 ? launch_diff_rows<128, true>(p, plan, s) : launch_diff_rows<128, false>(p, plan, s);

@@ -3,18 +3,24 @@
 //
 // The same mathematics as fa_diff_fwd.cuh. With R = (H / Hk) * Sq rows per key
 // head and R small, the call is bound by reading K_1, K_2 and V once, so the
-// kernel is built around that stream: the keys are cut into `n_split` runs,
-// one CTA per (batch, key head, run, 16 rows). All rows that share a key head
-// form one 16-row operand of m16n8k16 products, so shared heads read their
+// kernel is built around that stream. The lengths of the sequences are known on
+// the device only, so the work is cut there: all keys of all batch entries, in
+// units of 64, form one line that is divided evenly among teams of CTAs, one CTA
+// of a team per (key head, 16 rows). A team's stretch of the line covers a run
+// of keys of one batch entry, or of a few neighbouring ones ("pieces"); its CTAs
+// read neighbouring heads of the same keys, which lie side by side in memory.
+// All rows that share a key head form one 16-row operand of m16n8k16 products, so shared heads read their
 // keys once. A CTA has four streams of two warps, one warp per map. Each stream
 // takes every fourth 16-key tile through a ring of NS stages filled by TMA (a
 // lane of its first warp issues the loads; both warps wait on the stage's
 // mbarrier and hand it back through another: no producer warp, no block-wide
 // barrier in the loop), and each warp keeps its map's running maximum, sum and
-// unnormalised O. The streams' results join in shared memory, the runs' in a
+// unnormalised O. The streams' results join in shared memory, the pieces' in a
 // second small kernel (fa_diff_rows_join), both by the online softmax's
 // rescaling. Two CTAs share an SM, so one's start and end overlap the other's
-// stream. (One warp for both maps: 4 warps of 253 registers, XX us slower.)
+// stream. Calls of many batch entries and heads, or of short caches, need no
+// second kernel: one CTA takes all keys of its entry and writes the result
+// ("direct").
 //
 // P is split into two 16-bit terms, p = hi + lo, and multiplied with V twice:
 // the tensor cores have time to spare here, and O keeps the fp32 accuracy of P.
@@ -41,11 +47,50 @@ struct DiffRowsArgs {
   float scale_log2;
   int causal;
   int R, n_mt;   // query rows of a key head, ceil(R / 16)
-  int chunk;     // keys of one run, a multiple of 64
-  int n_split;   // runs
-  float* part_o;    // [b, hk, row][n_split][2][DV]: a run's unnormalised O_c
-  float2* part_ml;  // [b, hk, row][n_split][2]: its (m, l)
+  int teams;     // 0: direct
+  // A piece (batch entry b, team t) has slot b + t: along the line one of the two
+  // grows from piece to piece.
+  float* part_o;    // [slot][hk, row][2][DV]: a piece's unnormalised O_c
+  float2* part_ml;  // [slot][hk, row][2]: its (m, l)
 };
+
+// The line of 64-key units. Every lane of a warp calls these together.
+__device__ __forceinline__ int64_t rows_units(const DiffRowsArgs& a, int b) {
+  return b < a.B ? (diff_keys(a.k_lens, b, a.Sk) + 63) / 64 : 0;
+}
+__device__ __forceinline__ int64_t rows_warp_sum(int64_t v) {
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+  return v;
+}
+// Units of the batch entries before `b`.
+__device__ __forceinline__ int64_t rows_before(const DiffRowsArgs& a, int b) {
+  if (a.k_lens == nullptr) return static_cast<int64_t>(b) * ((a.Sk + 63) / 64);
+  int64_t v = 0;
+  for (int x = threadIdx.x & 31; x < b; x += 32) v += rows_units(a, x);
+  return rows_warp_sum(v);
+}
+// Teams that get work: each at least two units.
+__device__ __forceinline__ int rows_teams(const DiffRowsArgs& a, int64_t total) {
+  return static_cast<int>(min(static_cast<int64_t>(a.teams), max(static_cast<int64_t>(1), (total + 1) / 2)));
+}
+// The batch entry that holds unit `at` of the line, and the units before it.
+__device__ __forceinline__ int rows_find(const DiffRowsArgs& a, int64_t at, int64_t& before) {
+  before = 0;
+  for (int base = 0; base < a.B; base += 32) {
+    const int64_t mine = rows_units(a, base + static_cast<int>(threadIdx.x & 31));
+    const int64_t all = rows_warp_sum(mine);
+    if (at < before + all) {
+      for (int x = 0; x < 32; ++x) {  // which of the 32
+        const int64_t u = __shfl_sync(0xffffffffu, mine, x);
+        if (at < before + u) return base + x;
+        before += u;
+      }
+    }
+    before += all;
+  }
+  return a.B;
+}
 
 template <int DV>
 struct DiffRowsLayout {
@@ -130,19 +175,22 @@ __global__ void __launch_bounds__(256, 2)
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;  // fragment row group and column pair
 
-  // Heads before runs: the CTAs that run together read neighbouring heads of the
-  // same keys, which lie side by side in memory.
   const int mt = static_cast<int>(blockIdx.x) % a.n_mt;
   const int hk = static_cast<int>(blockIdx.x) / a.n_mt % a.Hk;
-  const int split = static_cast<int>(blockIdx.x) / a.n_mt / a.Hk % a.n_split;
-  const int b = static_cast<int>(blockIdx.x) / a.n_mt / a.Hk / a.n_split;
-  const int bk = b * a.Hk + hk;
+  const int team = static_cast<int>(blockIdx.x) / a.n_mt / a.Hk;  // direct: the batch entry
   const int group = a.H / a.Hk;
-  const int len = diff_keys(a.k_lens, b, a.Sk);
-  const int lo = split * a.chunk, hi = min(len, lo + a.chunk);
-  const int tiles = hi > lo ? (hi - lo + KT - 1) / KT : 0;
-  const int mine = tiles > stream ? (tiles - stream + 3) / 4 : 0;  // this stream's tiles: stream, stream + 4, ...
-  checked(b < a.B && mt * 16 < a.R, 601);
+  const bool direct = a.teams == 0;
+  // The stretch of the line: units [at, end), `before` the units of entries before b.
+  int b = team;
+  int64_t at = 0, end = 1, before = 0;
+  if (!direct) {
+    const int64_t total = rows_before(a, a.B);
+    const int teams = rows_teams(a, total);
+    at = team < teams ? total * team / teams : 0;
+    end = team < teams ? total * (team + 1) / teams : 0;
+    if (at < end) b = rows_find(a, at, before);
+    if (b >= a.B) at = end;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4 * NS; ++i) {
@@ -158,242 +206,270 @@ __global__ void __launch_bounds__(256, 2)
   uint64_t* full = bars + stream * NS;
   uint64_t* empty = bars + (4 + stream) * NS;
   uint8_t* ring = smem + stream * NS * L::TILE;
-  auto issue = [&](int i) {  // one lane: tile i of this stream into its stage
-    const int st = i % NS, key = lo + (stream + 4 * i) * KT;
-    uint8_t* dst = ring + st * L::TILE;
-    checked(key < a.Sk, 602);
-    mbar_arrive_expect_tx(&full[st], L::TILE);
-    tma_load_4d(dst, &tmK1, &full[st], 0, key, hk, b);
-    tma_load_4d(dst + KT * 128, &tmK2, &full[st], 0, key, hk, b);
-#pragma unroll
-    for (int vb = 0; vb < L::VB; ++vb) tma_load_4d(dst + (2 + vb) * KT * 128, &tmV, &full[st], vb * 64, key, hk, b);
-  };
-  const bool loads = c == 0 && lane == 0;
-  int issued = 0;
-  if (loads)
-    for (; issued < min(NS, mine); ++issued) issue(issued);
-
-  // Row r of the tile: query row i = r % Sq of head hk * group + r / Sq.
-  int lim[2];  // last key that rows g and g + 8 see
-  uint32_t qf[4][4];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = mt * 16 + g + 8 * e;
-    const int i = r % a.Sq, h = hk * group + r / a.Sq;
-    lim[e] = a.causal && r < a.R ? i + len - a.Sq : len - 1;  // rows past R are not written
-    const uint16_t* p = (c ? a.q[1] : a.q[0]) + b * a.q_s[c][0] + i * a.q_s[c][1] + h * a.q_s[c][2];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int col = ks * 16 + x * 8 + 2 * tq;
-        qf[ks][2 * x + e] = r < a.R && col < a.d ? *reinterpret_cast<const uint32_t*>(p + col) : 0u;
-      }
-  }
-  const int min_lim = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
   const float sl2 = a.scale_log2;
   // ldmatrix row addresses: K, matrices = 16-byte chunks 0-3 of 8 keys; V,
   // matrices = (keys 0-7, 8-15) x (chunk, chunk + 1), transposed.
   const int kr = lane & 7, km = lane >> 3;
   const int vr = (km & 1) * 8 + kr, vm = km >> 1;
+  int used = 0;  // tiles of this stream in earlier pieces
 
-  bool ok = true;
-  for (int i = 0; i < mine; ++i) {
-    const int st = i % NS, key0 = lo + (stream + 4 * i) * KT;
-    if (!(ok = __all_sync(0xffffffffu, wait_bar_c(&full[st], (i / NS) & 1, abort_flag, kRoleSoftmax, i)))) break;
-    uint8_t* tile = ring + st * L::TILE;
-    const uint32_t sk = smem_u32(tile) + c * KT * 128, sv = smem_u32(tile) + 2 * KT * 128;
-    if (key0 + KT > len) {
-      // Rows past the end count nothing, whatever they hold. (Both warps of the
-      // stream write the same zeros, each for itself; it is the last tile.)
-      for (int x = lane; x < L::VB * KT * 8; x += 32)
-        if (key0 + ((x >> 3) & (KT - 1)) >= len) st_shared_v4(sv + x * 16, 0, 0, 0, 0);
-      __syncwarp();
-    }
-    float s[2][4];
+  while (at < end) {
+    const int len = diff_keys(a.k_lens, b, a.Sk);
+    const int64_t units = (len + 63) / 64;
+    const int lo = direct ? 0 : static_cast<int>(at - before) * 64;
+    const int hi = direct ? len : static_cast<int>(min(static_cast<int64_t>(len), (end - before) * 64));
+    const int tiles = hi > lo ? (hi - lo + KT - 1) / KT : 0;
+    const int mine = tiles > stream ? (tiles - stream + 3) / 4 : 0;  // this stream's tiles: stream, stream + 4, ...
+    checked(b < a.B && mt * 16 < a.R, 601);
+    auto issue = [&](int i) {  // one lane: tile i of this stream into its stage
+      const int st = (used + i) % NS, key = lo + (stream + 4 * i) * KT;
+      uint8_t* dst = ring + st * L::TILE;
+      checked(key < a.Sk, 602);
+      mbar_arrive_expect_tx(&full[st], L::TILE);
+      tma_load_4d(dst, &tmK1, &full[st], 0, key, hk, b);
+      tma_load_4d(dst + KT * 128, &tmK2, &full[st], 0, key, hk, b);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      const int row = n * 8 + kr;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t f[4];
-        ldsm_x4(f, sk + row * 128 + (((hf * 4 + km) ^ (row & 7)) << 4));
-        mma16816<BF16>(s[n], qf[2 * hf], f[0], f[1]);
-        mma16816<BF16>(s[n], qf[2 * hf + 1], f[2], f[3]);
-      }
-    }
-    const bool masked = key0 + KT - 1 > min_lim;
-    uint32_t ph[4], pl[4];
+      for (int vb = 0; vb < L::VB; ++vb) tma_load_4d(dst + (2 + vb) * KT * 128, &tmV, &full[st], vb * 64, key, hk, b);
+    };
+    const bool loads = c == 0 && lane == 0;
+    int issued = 0;
+    if (loads)
+      for (; issued < min(NS, mine); ++issued) issue(issued);
+
+    // Row r of the tile: query row i = r % Sq of head hk * group + r / Sq.
+    int lim[2];  // last key that rows g and g + 8 see
+    uint32_t qf[4][4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (masked) {
+      const int r = mt * 16 + g + 8 * e;
+      const int i = r % a.Sq, h = hk * group + r / a.Sq;
+      lim[e] = a.causal && r < a.R ? i + len - a.Sq : len - 1;  // rows past R are not written
+      const uint16_t* p = (c ? a.q[1] : a.q[0]) + b * a.q_s[c][0] + i * a.q_s[c][1] + h * a.q_s[c][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (key0 + n * 8 + 2 * tq + x > lim[e]) s[n][2 * e + x] = -INFINITY;
-      }
-      float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      mx *= sl2;
-      // As in the other forwards, a stale maximum is kept within 2^8.
-      const bool raise = mx > m[e] + 8.f;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float alpha = raise ? ex2(m[e] - mx) : 1.f;
-        if (raise) m[e] = mx;
-        l[e] *= alpha;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n][2 * e] *= alpha;
-          acc[n][2 * e + 1] *= alpha;
+        for (int x = 0; x < 2; ++x) {
+          const int col = ks * 16 + x * 8 + 2 * tq;
+          qf[ks][2 * x + e] = r < a.R && col < a.d ? *reinterpret_cast<const uint32_t*>(p + col) : 0u;
         }
-      }
-      const float mu = m[e] == -INFINITY ? 0.f : m[e];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float p0 = ex2(fmaf(s[n][2 * e], sl2, -mu)), p1 = ex2(fmaf(s[n][2 * e + 1], sl2, -mu));
-        l[e] += p0 + p1;
-        const uint32_t w = pack2<BF16>(p0, p1);
-        const float2 r = unpack2<BF16>(w);
-        ph[2 * n + e] = w;
-        pl[2 * n + e] = pack2<BF16>(p0 - r.x, p1 - r.y);
-      }
     }
-#pragma unroll
-    for (int n = 0; n < NT; n += 2) {
-      uint32_t f[4];
-      ldsm_x4_t(f, sv + (n >> 3) * KT * 128 + vr * 128 + ((((n & 7) + vm) ^ (vr & 7)) << 4));
-      mma16816<BF16>(acc[n], ph, f[0], f[1]);
-      mma16816<BF16>(acc[n + 1], ph, f[2], f[3]);
-      mma16816<BF16>(acc[n], pl, f[0], f[1]);
-      mma16816<BF16>(acc[n + 1], pl, f[2], f[3]);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
-    if (loads && i + NS < mine) {
-      // The other map's warp is at most a tile behind in the same stage.
-      if (!wait_bar_c(&empty[st], (i / NS) & 1, abort_flag, kRoleLoader, i)) break;  // the abort flag is up
-      issue(i + NS);
-      ++issued;
-    }
-  }
-  if (loads && *abort_flag)  // let the copies already issued land before the CTA exits
-    for (int x = max(0, issued - NS); x < issued; ++x) drain_wait(&full[x % NS], (x / NS) & 1);
-  __syncwarp();
-  __syncthreads();  // every warp has read its last tile: the ring becomes the join's buffer
-  if (*abort_flag) return;
-
-  float* jo = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float s = l[e];
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if (tq == 0) ml[(stream * 2 + c) * 16 + g + 8 * e] = make_float2(m[e], s);
-    float* row = jo + ((stream * 2 + c) * 16 + g + 8 * e) * L::OROW;
+    const int min_lim = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g, g + 8
+    float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      *reinterpret_cast<float2*>(row + n * 8 + 2 * tq) = make_float2(acc[n][2 * e], acc[n][2 * e + 1]);
-  }
-  __syncthreads();
-  // Rows of the tile x groups of 4 columns over the block's threads.
-  for (int x = threadIdx.x; x < 16 * (DV / 4); x += 256) {
-    const int tr = x / (DV / 4), col = x % (DV / 4) * 4;
-    const int r = mt * 16 + tr;
-    if (r >= a.R) break;
-    float o[2][4], mm[2], ll[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {  // both maps
-      float top = -INFINITY;
+      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    for (int i = 0; i < mine; ++i) {
+      const int st = (used + i) % NS, key0 = lo + (stream + 4 * i) * KT;
+      const uint32_t ph_st = ((used + i) / NS) & 1;
+      if (!__all_sync(0xffffffffu, wait_bar_c(&full[st], ph_st, abort_flag, kRoleSoftmax, i))) break;
+      uint8_t* tile = ring + st * L::TILE;
+      const uint32_t sk = smem_u32(tile) + c * KT * 128, sv = smem_u32(tile) + 2 * KT * 128;
+      if (key0 + KT > len) {
+        // Rows past the end count nothing, whatever they hold. (Both warps of the
+        // stream write the same zeros, each for itself; it is the last tile.)
+        for (int x = lane; x < L::VB * KT * 8; x += 32)
+          if (key0 + ((x >> 3) & (KT - 1)) >= len) st_shared_v4(sv + x * 16, 0, 0, 0, 0);
+        __syncwarp();
+      }
+      float s[2][4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[(w * 2 + c) * 16 + tr].x);
-      mm[c] = top;
-      ll[c] = 0.f;
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        const int row = n * 8 + kr;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t f[4];
+          ldsm_x4(f, sk + row * 128 + (((hf * 4 + km) ^ (row & 7)) << 4));
+          mma16816<BF16>(s[n], qf[2 * hf], f[0], f[1]);
+          mma16816<BF16>(s[n], qf[2 * hf + 1], f[2], f[3]);
+        }
+      }
+      const bool masked = key0 + KT - 1 > min_lim;
+      uint32_t ph[4], pl[4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 v = ml[(w * 2 + c) * 16 + tr];
-        const float k = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2(v.x - top);  // a NaN sum stays one
-        ll[c] += v.y * k;
-        const float4 y = *reinterpret_cast<const float4*>(jo + ((w * 2 + c) * 16 + tr) * L::OROW + col);
-        o[c][0] = fmaf(y.x, k, o[c][0]);
-        o[c][1] = fmaf(y.y, k, o[c][1]);
-        o[c][2] = fmaf(y.z, k, o[c][2]);
-        o[c][3] = fmaf(y.w, k, o[c][3]);
+      for (int e = 0; e < 2; ++e) {
+        if (masked) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (key0 + n * 8 + 2 * tq + x > lim[e]) s[n][2 * e + x] = -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx *= sl2;
+        // As in the other forwards, a stale maximum is kept within 2^8.
+        const bool raise = mx > m[e] + 8.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? ex2(m[e] - mx) : 1.f;
+          if (raise) m[e] = mx;
+          l[e] *= alpha;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[n][2 * e] *= alpha;
+            acc[n][2 * e + 1] *= alpha;
+          }
+        }
+        const float mu = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = ex2(fmaf(s[n][2 * e], sl2, -mu)), p1 = ex2(fmaf(s[n][2 * e + 1], sl2, -mu));
+          l[e] += p0 + p1;
+          const uint32_t w = pack2<BF16>(p0, p1);
+          const float2 r = unpack2<BF16>(w);
+          ph[2 * n + e] = w;
+          pl[2 * n + e] = pack2<BF16>(p0 - r.x, p1 - r.y);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t f[4];
+        ldsm_x4_t(f, sv + (n >> 3) * KT * 128 + vr * 128 + ((((n & 7) + vm) ^ (vr & 7)) << 4));
+        mma16816<BF16>(acc[n], ph, f[0], f[1]);
+        mma16816<BF16>(acc[n + 1], ph, f[2], f[3]);
+        mma16816<BF16>(acc[n], pl, f[0], f[1]);
+        mma16816<BF16>(acc[n + 1], pl, f[2], f[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (loads && i + NS < mine) {
+        // The other map's warp is at most a tile behind in the same stage.
+        if (!wait_bar_c(&empty[st], ph_st, abort_flag, kRoleLoader, i)) break;  // the abort flag is up
+        issue(i + NS);
+        ++issued;
       }
     }
-    const int row = r % a.Sq, h = hk * group + r / a.Sq;
-    if (a.n_split == 1) {
-      const bool has = len > 0 && (!a.causal || row + len - a.Sq >= 0);
-      diff_row_out<4, BF16>(a, b, h, row, col, has, o[0], o[1], ll[0], ll[1]);
-      if (col == 0)
+    if (loads && *abort_flag)  // let the copies already issued land before the CTA exits
+      for (int x = used + max(0, issued - NS); x < used + issued; ++x) drain_wait(&full[x % NS], (x / NS) & 1);
+    used += mine;
+    __syncwarp();
+    __syncthreads();  // every warp has read its last tile: the ring becomes the join's buffer
+    if (*abort_flag) return;
+
+    float* jo = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          a.lse[((static_cast<int64_t>(c) * a.B + b) * a.H + h) * a.Sq + row] =
-              has ? (mm[c] + __log2f(ll[c])) * 0.69314718055994531f : -INFINITY;
-    } else {
-      const int64_t slot = (static_cast<int64_t>(bk) * a.R + r) * a.n_split + split;
-      checked(slot < static_cast<int64_t>(a.B) * a.Hk * a.R * a.n_split, 603);
+    for (int e = 0; e < 2; ++e) {
+      float s = l[e];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (tq == 0) ml[(stream * 2 + c) * 16 + g + 8 * e] = make_float2(m[e], s);
+      float* row = jo + ((stream * 2 + c) * 16 + g + 8 * e) * L::OROW;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        *reinterpret_cast<float4*>(a.part_o + (slot * 2 + c) * DV + col) =
-            make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
-        if (col == 0) a.part_ml[slot * 2 + c] = make_float2(mm[c], ll[c]);
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(row + n * 8 + 2 * tq) = make_float2(acc[n][2 * e], acc[n][2 * e + 1]);
+    }
+    __syncthreads();
+    // Rows of the tile x groups of 4 columns over the block's threads.
+    for (int x = threadIdx.x; x < 16 * (DV / 4); x += 256) {
+      const int tr = x / (DV / 4), col = x % (DV / 4) * 4;
+      const int r = mt * 16 + tr;
+      if (r >= a.R) break;
+      float o[2][4], mm[2], ll[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // both maps
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[(w * 2 + c) * 16 + tr].x);
+        mm[c] = top;
+        ll[c] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 v = ml[(w * 2 + c) * 16 + tr];
+          const float k = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2(v.x - top);  // a NaN sum stays one
+          ll[c] += v.y * k;
+          const float4 y = *reinterpret_cast<const float4*>(jo + ((w * 2 + c) * 16 + tr) * L::OROW + col);
+          o[c][0] = fmaf(y.x, k, o[c][0]);
+          o[c][1] = fmaf(y.y, k, o[c][1]);
+          o[c][2] = fmaf(y.z, k, o[c][2]);
+          o[c][3] = fmaf(y.w, k, o[c][3]);
+        }
+      }
+      const int row = r % a.Sq, h = hk * group + r / a.Sq;
+      if (direct) {
+        const bool has = len > 0 && (!a.causal || row + len - a.Sq >= 0);
+        diff_row_out<4, BF16>(a, b, h, row, col, has, o[0], o[1], ll[0], ll[1]);
+        if (col == 0)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            a.lse[((static_cast<int64_t>(c) * a.B + b) * a.H + h) * a.Sq + row] =
+                has ? (mm[c] + __log2f(ll[c])) * 0.69314718055994531f : -INFINITY;
+      } else {
+        const int64_t slot = (static_cast<int64_t>(b + team) * a.Hk + hk) * a.R + r;
+        checked(slot < static_cast<int64_t>(a.B + a.teams) * a.Hk * a.R, 603);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          *reinterpret_cast<float4*>(a.part_o + (slot * 2 + c) * DV + col) =
+              make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+          if (col == 0) a.part_ml[slot * 2 + c] = make_float2(mm[c], ll[c]);
+        }
       }
     }
+    // On to the next batch entry of the stretch.
+    at = before + units;
+    if (direct || at >= end) break;
+    before = at;
+    ++b;
+    while (b < a.B && rows_units(a, b) == 0) ++b;
+    if (b >= a.B) break;
+    fence_proxy_async_smem();  // the join's buffer becomes the ring again
+    __syncthreads();
   }
 }
 
-// Joins the runs of one row per block. Eight warps take every eighth run each
-// (a lane holds DV / 32 columns of both maps), then meet in shared memory.
+// Joins the pieces of one row per block. Eight warps take every eighth piece
+// each (a lane holds DV / 32 columns of both maps), then meet in shared memory.
 template <int DV, bool BF16>
 __global__ void __launch_bounds__(256) fa_diff_rows_join(const DiffRowsArgs a) {
   using namespace sm100;
   constexpr int N = DV / 32;
   __shared__ float so[8][2][DV];
   __shared__ float2 sml[8][2];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' results are written and visible
-  const int64_t at = blockIdx.x;  // (b, hk, r)
-  const int r = static_cast<int>(at % a.R);
-  const int bk = static_cast<int>(at / a.R);
-  const int b = bk / a.Hk;
-  const int row = r % a.Sq, h = bk % a.Hk * (a.H / a.Hk) + r / a.Sq;
+  const int r = static_cast<int>(blockIdx.x) % a.R;
+  const int hk = static_cast<int>(blockIdx.x) / a.R % a.Hk;
+  const int b = static_cast<int>(blockIdx.x) / a.R / a.Hk;
+  const int row = r % a.Sq, h = hk * (a.H / a.Hk) + r / a.Sq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = diff_keys(a.k_lens, b, a.Sk);
-  const int used = (len + a.chunk - 1) / a.chunk;  // later runs have no key
-  const float2* pml = a.part_ml + at * a.n_split * 2;
-  const float* po = a.part_o + at * a.n_split * 2 * DV + lane * N;
+  // The teams that hold this entry's units [u0, u1): team t starts at unit
+  // floor(total t / teams), so unit u lies with team ceil((u + 1) teams / total) - 1.
+  const int64_t total = rows_before(a, a.B), u0 = rows_before(a, b), u1 = u0 + rows_units(a, b);
+  const int teams = rows_teams(a, total);
+  int t0 = 0, t1 = -1;
+  if (u1 > u0 && total >= u1) {
+    t0 = static_cast<int>(((u0 + 1) * teams + total - 1) / total) - 1;
+    t1 = min(static_cast<int>((u1 * teams + total - 1) / total) - 1, teams - 1);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written and visible
+  // Team t's piece: slot b + t.
+  auto at = [&](int t) { return (static_cast<int64_t>(b + t) * a.Hk + hk) * a.R + r; };
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][N];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int e = 0; e < N; ++e) o[c][e] = 0.f;
-  // The row's maxima first, so that the runs' O are added without rescaling.
-  for (int s = lane; s < used; s += 32)
+  // The row's maxima first, so that the pieces' O are added without rescaling.
+  for (int t = t0 + lane; t <= t1; t += 32)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) m[c] = fmaxf(m[c], pml[s * 2 + c].x);
+    for (int c = 0; c < 2; ++c) m[c] = fmaxf(m[c], a.part_ml[at(t) * 2 + c].x);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], x));
 #pragma unroll 4
-  for (int s = warp; s < used; s += 8)
+  for (int t = t0 + warp; t <= t1; t += 8)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const float2 v = pml[s * 2 + c];
+      const float2 v = a.part_ml[at(t) * 2 + c];
       const float k = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2(v.x - m[c]);
       l[c] += v.y * k;
+      const float* po = a.part_o + (at(t) * 2 + c) * DV + lane * N;
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[c][e] = fmaf(po[(static_cast<int64_t>(s) * 2 + c) * DV + e], k, o[c][e]);
+      for (int e = 0; e < N; ++e) o[c][e] = fmaf(po[e], k, o[c][e]);
     }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {

@@ -200,6 +200,26 @@ def test_few_rows(fa_lib, c):
     close_in_norm("o", o, want["o"], 4 * u)
 
 
+def test_many_ragged_lengths(fa_lib):
+    """Stretches of the line that cross batch entries, entries of length 0 among them, in a row and at the ends."""
+    g = torch.Generator().manual_seed(5)
+    for B, Sq, Sk, H, Hk, low in ((70, 1, 900, 4, 2, 0), (33, 2, 400, 3, 1, 300), (5, 1, 2600, 16, 16, 0)):
+        lens = torch.randint(low, Sk + 1, (B,), generator=g, dtype=torch.int32)
+        lens[torch.randint(0, B, (B // 4,), generator=g)] = 0
+        lens[0] = lens[-1] = 0
+        u, t = ROUND[torch.float16]
+        q, k, v, lam, _ = case(B, Sq, Sk, H, Hk, 64, 64, torch.float16, B, "head", torch.float32)
+        want = differential(np64(q), np64(k), np64(v), np64(lam), 0.125, True, n_keys=lens.tolist(), u=u, t=t)
+        o, lse, _ = fa.diff_forward(q.cuda(), k.cuda(), v.cuda(), lam.cuda(), causal=True, k_lens=lens.cuda())
+        status_clear()
+        check_lse(lse, want["lse"])
+        within("o", o, want["o"], want["o_bound"])
+    # no keys at all
+    o, lse, _ = fa.diff_forward(q.cuda(), k.cuda(), v.cuda(), lam.cuda(), k_lens=torch.zeros_like(lens).cuda())
+    status_clear()
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
 def test_autograd_against_differences(fa_lib):
     """The gradients against central differences of the oracle along random directions."""
     c = case(1, 70, 90, 2, 1, 64, 128, torch.float16, 31, "head", torch.float32)
