@@ -309,6 +309,8 @@ int launch_diff_bwd(const fa_diff_bwd_params* p, cudaStream_t stream) {
   a.dq_part = p->deterministic ? reinterpret_cast<float*>(ws) : nullptr;
   a.vec = reinterpret_cast<float*>(ws + w.off_vec);
   a.drow = reinterpret_cast<float*>(ws + w.off_drow);
+  const fa_diff_lambda& lam = p->lambda;
+  if (lam.extent_b == p->B && lam.extent_s == p->Sq && lam.extent_h == p->H) a.dlam = p->dlambda;
   a.parts = w.parts;
   a.dkv_part = w.parts > 1 ? reinterpret_cast<float*>(ws + w.off_dkv) : nullptr;
   const int64_t rows = int64_t(p->B) * p->H * a.Sq_pad;
@@ -330,7 +332,7 @@ int launch_diff_bwd(const fa_diff_bwd_params* p, cudaStream_t stream) {
   else
     fa::fa_diff_dq<BF16, false><<<dq_grid, 256, 0, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return launch_lam(p, a.drow, reinterpret_cast<float*>(ws + w.off_part), stream);
+  return a.dlam != nullptr ? FA_OK : launch_lam(p, a.drow, reinterpret_cast<float*>(ws + w.off_part), stream);
 }
 
 template <bool BF16>

@@ -14,7 +14,7 @@
 // Kernels on the caller's stream:
 //  1. fa_diff_pre: per row Delta_1, Delta_2, both LSEs in base 2 (+inf for rows
 //     with no key and padding rows) and -lambda, packed per 64 rows; zeroes
-//     the fp32 dQ accumulators; writes -Delta_2 per row for dlambda.
+//     the fp32 dQ accumulators; writes dlambda, or the terms of its sums.
 //  2. fa_diff_bwd_main: one CTA per (batch, key head, 128-key block); walks the
 //     query blocks of every query head that shares the key head, so dK and dV
 //     of shared heads are summed in the CTA's fp32 accumulators, in a fixed
@@ -22,31 +22,43 @@
 //     (few key heads, many query heads, a causal mask), the lists are cut into
 //     parts, a CTA each, whose fp32 dK and dV fa_diff_dkv adds in order.
 //  3. fa_diff_dq: dq_c = scale * accumulator, rounded to the input dtype.
-//  4. fa_diff_lam_few, or fa_diff_lam_part and fa_diff_lam_sum: dlambda, summed over the axes lambda
-//     is broadcast over in a fixed order.
+//  4. fa_diff_lam_few, or fa_diff_lam_part and fa_diff_lam_sum: dlambda summed
+//     over the axes lambda is broadcast over, in a fixed order.
 //
 // Main kernel. Query rows go through the softmax 64 at a time ("chunks", two
 // per 128-row query block): S_1^T, S_2^T and dP^T of a chunk then take 3 x 64
 // columns of tensor memory beside the accumulators dV, dK_1, dK_2 (256) and a
-// dQ block of one map (64 columns), 512 in all, and the shared memory holds
-// two stages of Q_1, Q_2 and dO. dQ is a product over whole 128-row blocks (M
-// = 128 is the tensor core's full rate), taken after the second chunk from the
-// two dS^T halves in shared memory.
+// dQ block of one map (64 columns), 512 in all. dQ is a product over whole
+// 128-row blocks (M = 128 is the tensor core's full rate), taken from the dS^T
+// halves of both chunks in shared memory.
 //
 // Warp roles (448 threads):
-//   warps 0-7   one key row per thread; warps 0-3 take query columns [0, 32)
-//               of the chunk, warps 4-7 [32, 64). P_1 and -lambda P_2 stay in
-//               fp32 registers between the two phases of a chunk. At the end
-//               warps 0-3 write dK_1 and dK_2, warps 4-7 dV.
+//   warps 0-7   P and dS of 32 keys x 32 query columns per warp (warps 0-3 take
+//               the chunk's columns [0, 32), warps 4-7 [32, 64)), in matrix-
+//               fragment order. P_1 and -lambda P_2 stay in fp32 registers
+//               between the two phases of a chunk. At the end warps 0-3 write
+//               dK_1 and dK_2, warps 4-7 dV.
 //   warps 8-11  read the dQ blocks out of tensor memory (one query row per
 //               thread) and add them into the fp32 accumulators through the
 //               TMA; deterministic mode stores them into their own slots.
-//   warp  12    TMA loader: K_1, K_2, V once; Q_1, Q_2 with the row terms, and
-//               dO, per chunk
+//   warp  12    TMA loader: K_1, K_2, V once; per chunk Q_1 and Q_2, dO, and
+//               the row terms
 //   warp  13    MMA issuer
 // MMA order per chunk i: dV(i), S_1(i+1), S_2(i+1), [dQ], dK_1(i), dK_2(i),
 // dP(i+1), with dQ_1 in odd chunks and dQ_2 in the even ones after them: the
 // softmax of chunk i+1 starts while dK(i), dP(i+1) and dQ run.
+//
+// What bounds it. A chunk's products take 1650 tensor cycles alone (1280 at
+// the full rate: with N = 64 both operands from shared memory are read at 128
+// bytes a cycle, 48 cycles an instruction instead of 32, which is why W^T and
+// dS^T go to dV and dK through tensor memory). The softmax's two phases take
+// about 2300 cycles a chunk and overlap the products except for the hand-offs
+// (W ready -> dV, S ready -> exponentials, dS ready -> dK). Measured at B = 1,
+// H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 455 us, 753 TFLOP/s, tensor
+// pipe 36% active. Without the exponentials the same grid takes 440 us, without
+// the dQ reductions 459 of 474: no single part carries the rest. Tried and
+// slower: 16 softmax warps of 16 columns (550 us), dQ_2 over dP's columns with
+// dK from shared memory (602), dQ by red.global instead of the TMA (604).
 #pragma once
 
 #include <type_traits>
@@ -70,7 +82,8 @@ struct DiffBwdArgs {
   int64_t o_s[3], o2_s[3], do_s[3], dq_s[2][3], dk_s[2][3], dv_s[3];
   float* dq_acc;   // fp32 [2][B*H][Sq_pad][64]
   float* vec;      // fp32 [B*H][Sq_pad / 64][5][64]: -lse2_1, -lse2_2, -lambda, -Delta_1, -Delta_2
-  float* drow;     // fp32 [B][H][Sq]: -Delta_2
+  float* drow;     // fp32 [B][H][Sq]: -Delta_2, where lambda is broadcast
+  void* dlam;      // dlambda [B][Sq][H], where it is not; else null
   float* dkv_part;  // parts > 1: fp32 [parts][B*Hk][Sk_pad][128 + DV]: a part's dK_1, dK_2, dV; else null
   float* dq_part;  // deterministic mode: fp32 [B*H][nqb][nkb][2][128][64] slots; else null
   int B, H, Hk, Sq, Sk, Sq_pad;
@@ -82,6 +95,14 @@ struct DiffBwdArgs {
 };
 
 constexpr int kDiffVec = 5 * 64;  // floats of one chunk's row terms
+
+__device__ __forceinline__ void store_lam(void* p, int kind, int64_t at, float v) {
+  if (kind == kLamF32)
+    static_cast<float*>(p)[at] = v;
+  else
+    static_cast<uint16_t*>(p)[at] =
+        static_cast<uint16_t>((kind == kLamBF16 ? sm100::pack2<true>(v, 0.f) : sm100::pack2<false>(v, 0.f)) & 0xffffu);
+}
 
 // Tensor memory in matrix-fragment order: of a warp's 32 lanes x 8 columns,
 // thread t gets rows t / 4 + {0, 8, 16, 24} and columns 2 (t % 4) + {0, 1}, where
@@ -198,7 +219,10 @@ __global__ void __launch_bounds__(256) fa_diff_pre(const DiffBwdArgs a) {
       } else {
         d_o = d_2 = 0.f;
       }
-      a.drow[at] = -d_2;
+      if (a.dlam != nullptr)
+        store_lam(a.dlam, a.lam_kind, (static_cast<int64_t>(b) * a.Sq + i) * a.H + h, -d_2);
+      else
+        a.drow[at] = -d_2;
     }
     float* v = a.vec + (static_cast<int64_t>(bh) * (a.Sq_pad / 64) + i / 64) * kDiffVec + (i & 63);
     v[0] = -l1;
@@ -321,14 +345,6 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
   return r;
 }
 
-__device__ __forceinline__ void store_lam(void* p, int kind, int64_t at, float v) {
-  if (kind == kLamF32)
-    static_cast<float*>(p)[at] = v;
-  else
-    static_cast<uint16_t*>(p)[at] =
-        static_cast<uint16_t>((kind == kLamBF16 ? sm100::pack2<true>(v, 0.f) : sm100::pack2<false>(v, 0.f)) & 0xffffu);
-}
-
 // Term k of element x's sum. The summed axes, innermost first: rows, heads, batch.
 __device__ __forceinline__ float lam_term(const LamSumArgs& a, int64_t x, int64_t k) {
   const int eh = static_cast<int>(x % a.ext[2]);
@@ -340,7 +356,7 @@ __device__ __forceinline__ float lam_term(const LamSumArgs& a, int64_t x, int64_
   return a.drow[((eb + b) * a.H + eh + h) * a.Sq + es + s];
 }
 
-// Few terms (one, where no axis is broadcast): one thread per element.
+// Few terms: one thread per element.
 __global__ void __launch_bounds__(256) fa_diff_lam_few(const LamSumArgs a) {
   const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (x >= a.n_out) return;
