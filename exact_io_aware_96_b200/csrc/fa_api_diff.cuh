@@ -29,11 +29,20 @@ int check_axes(const fa_tensor& t, int B, int S, int H) {
   return FA_OK;
 }
 
+// The stride of an axis of extent 1 is never stepped over and may be anything
+// (torch leaves odd ones there): it becomes 0 before the checks.
+void one_step(fa_tensor& t, int B, int S, int H) {
+  if (B == 1) t.stride_b = 0;
+  if (S == 1) t.stride_s = 0;
+  if (H == 1) t.stride_h = 0;
+}
+
 int check_diff(int B, int H, int Hk, int Sq, int Sk, int D, int Dv, float scale, int causal, int dtype) {
   int st = check_common(B, H, Sq, Sk, D, scale, causal, dtype);
   if (st != FA_OK) return st;
   if (D > 64 || Dv < 8 || Dv > 128 || Dv % 8) return FA_ERR_UNSUPPORTED;
   if (Hk < 1 || H % Hk) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * 1.4426950408889634f)) return FA_ERR_INVALID_ARG;  // the scale in base 2
   // Row indices of both maps' fp32 dQ accumulators are 32-bit tensor-map
   // coordinates, and grids are 31-bit.
   const int64_t lim = (int64_t(1) << 31) - 1;
@@ -401,18 +410,22 @@ size_t fa_diff_fwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, i
   return size_t(rows_plan(B, H, Hk, Sq, Sk, Dv).bytes);
 }
 
-int fa_diff_fwd(const fa_diff_fwd_params* p, fa_stream_t stream) {
-  if (p == nullptr) return FA_ERR_INVALID_ARG;
+int fa_diff_fwd(const fa_diff_fwd_params* given, fa_stream_t stream) {
+  if (given == nullptr) return FA_ERR_INVALID_ARG;
+  fa_diff_fwd_params args = *given;
+  const fa_diff_fwd_params* p = &args;
+  fa_tensor* qs[4] = {&args.q[0], &args.q[1], &args.o, &args.o2};
+  for (fa_tensor* t : qs) one_step(*t, p->B, p->Sq, p->H);
+  fa_tensor* ks[3] = {&args.k[0], &args.k[1], &args.v};
+  for (fa_tensor* t : ks) one_step(*t, p->B, p->Sk, p->Hk);
   int st = check_diff(p->B, p->H, p->Hk, p->Sq, p->Sk, p->D, p->Dv, p->scale, p->causal, p->dtype);
   if (st != FA_OK) return st;
-  for (int c = 0; c < 2; ++c) {
-    if ((st = check_view(p->q[c])) != FA_OK || (st = check_axes(p->q[c], p->B, p->Sq, p->H)) != FA_OK) return st;
-    if ((st = check_view(p->k[c])) != FA_OK || (st = check_axes(p->k[c], p->B, p->Sk, p->Hk)) != FA_OK) return st;
+  for (const fa_tensor* t : qs) {
+    if (t == &p->o2 && t->ptr == nullptr) continue;
+    if ((st = check_view(*t)) != FA_OK || (st = check_axes(*t, p->B, p->Sq, p->H)) != FA_OK) return st;
   }
-  if ((st = check_view(p->v)) != FA_OK || (st = check_axes(p->v, p->B, p->Sk, p->Hk)) != FA_OK) return st;
-  if ((st = check_view(p->o)) != FA_OK || (st = check_axes(p->o, p->B, p->Sq, p->H)) != FA_OK) return st;
-  if ((st = check_view(p->o2, true)) != FA_OK) return st;
-  if (p->o2.ptr != nullptr && (st = check_axes(p->o2, p->B, p->Sq, p->H)) != FA_OK) return st;
+  for (const fa_tensor* t : ks)
+    if ((st = check_view(*t)) != FA_OK || (st = check_axes(*t, p->B, p->Sk, p->Hk)) != FA_OK) return st;
   if ((st = check_lam(p->lambda, p->B, p->Sq, p->H, p->dtype)) != FA_OK) return st;
   if (p->lse == nullptr) return FA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(p->lse) & 3u) return FA_ERR_MISALIGNED;
@@ -436,16 +449,20 @@ size_t fa_diff_bwd_workspace_size(int B, int H, int Hk, int Sq, int Sk, int D, i
   return bytes > (uint64_t(1) << 50) ? 0 : size_t(bytes);
 }
 
-int fa_diff_bwd(const fa_diff_bwd_params* p, fa_stream_t stream) {
-  if (p == nullptr) return FA_ERR_INVALID_ARG;
+int fa_diff_bwd(const fa_diff_bwd_params* given, fa_stream_t stream) {
+  if (given == nullptr) return FA_ERR_INVALID_ARG;
+  fa_diff_bwd_params args = *given;
+  const fa_diff_bwd_params* p = &args;
+  fa_tensor* qs[7] = {&args.q[0], &args.q[1], &args.o, &args.o2, &args.dO, &args.dq[0], &args.dq[1]};
+  for (fa_tensor* t : qs) one_step(*t, p->B, p->Sq, p->H);
+  fa_tensor* ks[6] = {&args.k[0], &args.k[1], &args.v, &args.dk[0], &args.dk[1], &args.dv};
+  for (fa_tensor* t : ks) one_step(*t, p->B, p->Sk, p->Hk);
   int st = check_diff(p->B, p->H, p->Hk, p->Sq, p->Sk, p->D, p->Dv, p->scale, p->causal, p->dtype);
   if (st != FA_OK) return st;
-  const fa_tensor* qs[8] = {&p->q[0], &p->q[1], &p->o, &p->o2, &p->dO, &p->dq[0], &p->dq[1], nullptr};
-  for (int i = 0; qs[i] != nullptr; ++i)
-    if ((st = check_view(*qs[i])) != FA_OK || (st = check_axes(*qs[i], p->B, p->Sq, p->H)) != FA_OK) return st;
-  const fa_tensor* ks[7] = {&p->k[0], &p->k[1], &p->v, &p->dk[0], &p->dk[1], &p->dv, nullptr};
-  for (int i = 0; ks[i] != nullptr; ++i)
-    if ((st = check_view(*ks[i])) != FA_OK || (st = check_axes(*ks[i], p->B, p->Sk, p->Hk)) != FA_OK) return st;
+  for (const fa_tensor* t : qs)
+    if ((st = check_view(*t)) != FA_OK || (st = check_axes(*t, p->B, p->Sq, p->H)) != FA_OK) return st;
+  for (const fa_tensor* t : ks)
+    if ((st = check_view(*t)) != FA_OK || (st = check_axes(*t, p->B, p->Sk, p->Hk)) != FA_OK) return st;
   if ((st = check_lam(p->lambda, p->B, p->Sq, p->H, p->dtype)) != FA_OK) return st;
   if (p->dlambda == nullptr || p->lse == nullptr) return FA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(p->dlambda) & (p->lambda.dtype == FA_LAMBDA_FP32 ? 3u : 1u)) return FA_ERR_MISALIGNED;
@@ -459,8 +476,14 @@ int fa_diff_bwd(const fa_diff_bwd_params* p, fa_stream_t stream) {
   return p->dtype == FA_BF16 ? launch_diff_bwd<128, true>(p, s) : launch_diff_bwd<128, false>(p, s);
 }
 
-int fa_rotary(const fa_rotary_params* p, fa_stream_t stream) {
-  if (p == nullptr) return FA_ERR_INVALID_ARG;
+int fa_rotary(const fa_rotary_params* given, fa_stream_t stream) {
+  if (given == nullptr) return FA_ERR_INVALID_ARG;
+  fa_rotary_params args = *given;
+  const fa_rotary_params* p = &args;
+  one_step(args.q, p->B, p->S, p->H);
+  one_step(args.q_out, p->B, p->S, p->H);
+  one_step(args.k, p->B, p->S, p->Hk);
+  one_step(args.k_out, p->B, p->S, p->Hk);
   if (p->B < 1 || p->S < 1 || p->H < 1 || p->Hk < 0) return FA_ERR_INVALID_ARG;
   if (p->dtype != FA_FP16 && p->dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
   if (p->D < 8 || p->D > 256 || p->D % 8) return FA_ERR_UNSUPPORTED;

@@ -303,11 +303,12 @@ size_t fa_bwd_workspace_size_ex(int B, int H, int Sq, int Sk, int D, int determi
    Layout: q[c] [B, Sq, H, D], k[c] [B, Sk, Hk, D], v [B, Sk, Hk, Dv], o and o2
    [B, Sq, H, Dv]: strided views as in fa_fwd_ex, so q[0], q[1] may be the two
    slices of one [B, Sq, H, 2, D] tensor. An axis longer than 1 may not have
-   stride 0. Query head h reads key/value head h / (H / Hk); Hk divides H.
+   stride 0; the stride of an axis of length 1 is not read. Query head h reads key/value head h / (H / Hk); Hk divides H.
    head_dim: D a multiple of 8 in [8, 64], Dv a multiple of 8 in [8, 128];
    others are FA_ERR_UNSUPPORTED. dtype, scale, causal mask (bottom-right
    aligned), alignment, ownership, asynchrony and errors as for fa_fwd_ex;
-   2 * B * H * Sq (rounded up to 128) below 2^31. */
+   2 * B * H * Sq (rounded up to 128) below 2^31. The backward holds P_1 - lambda
+   P_2 in the call's type: with fp16, |lambda| has to stay below 65504. */
 
 /* lambda: one value per (batch, query row, head), or one for all of an axis
    whose extent is 1 (its stride is then not read). dtype: FA_LAMBDA_FP32, or

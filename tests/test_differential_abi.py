@@ -87,7 +87,7 @@ def bwd(**kw):
 SHARED = [
     (dict(q=tens(at=None)), -1), (dict(v=tens(at=None)), -1), (dict(lse=None), -1), (dict(lam=lam(ptr=None)), -1),
     (dict(B=0), -1), (dict(Hk=0), -1), (dict(H=3, lam=lam(extent_h=3)), -1), (dict(Sk=0), -1),
-    (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(causal=2), -1),
+    (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(scale=3e38), -1), (dict(causal=2), -1),
     (dict(D=72), -2), (dict(D=4), -2), (dict(Dv=136), -2), (dict(Dv=12), -2), (dict(dtype=2), -2),
     (dict(lam=lam(dtype=fa.FA_BF16)), -2), (dict(lam=lam(extent_h=3)), -1), (dict(lam=lam(stride_h=-1)), -1),
     (dict(lam=lam(ptr=A + 2)), -3), (dict(k=tens(at=A + 8)), -3), (dict(q=fa.FaTensor(A, 128 * 128, 130, 64)), -3),

@@ -262,6 +262,58 @@ def test_autograd_takes_what_programs_hand_it(fa_lib):
         assert torch.equal(diff_attn_func(q, k, v, lam), o)
 
 
+def test_strides_of_axes_of_length_one(fa_lib):
+    """torch calls a tensor contiguous whatever the stride of an axis of length 1."""
+    q, k, v, lam, do = (x.cuda() for x in case(1, 1, 200, 1, 1, 64, 128, torch.bfloat16, 47))
+    odd = lambda t: t.as_strided(t.shape, [1 if n == 1 else s for n, s in zip(t.shape, t.stride())])  # noqa: E731
+    o, lse, o2 = fa.diff_forward(q, k, v, lam, need_o2=True)
+    want = fa.diff_backward(q, k, v, lam, o, o2, lse, do, deterministic=True)
+    p, l2, p2 = fa.diff_forward(odd(q), odd(k), odd(v), lam, out=odd(torch.empty_like(o)), need_o2=True)
+    got = fa.diff_backward(odd(q), odd(k), odd(v), lam, odd(p), odd(p2), l2, odd(do), deterministic=True)
+    pos, f = torch.arange(200, device="cuda")[None], fa.rotary_inv_freq((32,))
+    r, s = fa.rotary(odd(k), None, pos, f)[0], fa.rotary(k, None, pos, f)[0]
+    status_clear()
+    assert torch.equal(o, p) and torch.equal(r, s) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_rotary_of_q_alone_with_gradient(fa_lib):
+    q = torch.randn((1, 30, 2, 64), device="cuda").half().requires_grad_()
+    pos, f = torch.arange(30, device="cuda")[None], fa.rotary_inv_freq((32,))
+    out, none = rotary_func(q, None, pos, f)
+    (g,) = torch.autograd.grad(out, q, torch.ones_like(out))
+    assert none is None
+    assert torch.equal(g, fa.rotary(torch.ones_like(q), None, pos, f, inverse=True)[0])
+
+
+FIRST_CALL = """
+import torch
+from exact_io_aware_96_b200 import fa
+q, k, v = (torch.randn(s, device="cuda").half() for s in ((1, {Sq}, 2, 2, 64), (1, 600, 2, 2, 64), (1, 600, 2, 128)))
+lam = torch.rand(2, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    o, lse, o2 = fa.diff_forward(q, k, v, lam, need_o2=True)
+    grads = fa.diff_backward(q, k, v, lam, o, o2, lse, o, deterministic=True)
+g.replay()
+torch.cuda.synchronize()
+p, l2, p2 = fa.diff_forward(q, k, v, lam, need_o2=True)
+assert torch.equal(o, p)
+assert all(torch.equal(a, b) for a, b in zip(grads, fa.diff_backward(q, k, v, lam, p, p2, l2, p, deterministic=True)))
+assert fa.fa_last_device_status()[0] == 0
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("Sq", [1, 200])
+def test_first_call_inside_a_capture(fa_lib, Sq):
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL.format(Sq=Sq)], cwd=root, capture_output=True, text=True,
+                         timeout=200)
+    assert "captured first" in out.stdout, out.stderr[-1500:]
+
+
 def test_no_second_derivative(fa_lib):
     q, k, v, lam, _ = (x.cuda() for x in case(1, 8, 8, 1, 1, 64, 64, torch.float16, 23))
     q.requires_grad_()
