@@ -94,66 +94,16 @@ class PackedQKVAttention(torch.nn.Module):
         return flash_attn_qkvpacked_func(qkv, self.causal, self.softmax_scale)
 
 
-def _strided_ready(t: torch.Tensor) -> torch.Tensor:
-    """`t`, or a dense copy if its strides, alignment or an expanded axis keep the kernels from reading it."""
-    if t.data_ptr() % 16 == 0 and t.is_contiguous():
-        return t
-    ok = (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
-          and all(s % 8 == 0 and (s > 0 or n == 1) for s, n in zip(t.stride()[:-1], t.shape[:-1])))
-    return t if ok else t.clone(memory_format=torch.contiguous_format)
-
-
-class DiffAttentionFunction(torch.autograd.Function):
-    """Differential attention. Saves q, k, v, lam, O, O_2 and both logsumexps;
-    the backward rebuilds both maps from the logsumexps."""
-
-    @staticmethod
-    def forward(ctx, q, k, v, lam, causal: bool, scale, deterministic: bool):
-        q, k, v = _strided_ready(q), _strided_ready(k), _strided_ready(v)
-        o, lse, o2 = fa.diff_forward(q, k, v, lam, causal=causal, scale=scale, need_o2=any(ctx.needs_input_grad))
-        ctx.save_for_backward(q, k, v, lam, o, o2, lse)
-        ctx.causal, ctx.scale, ctx.deterministic = causal, scale, deterministic
-        return o
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, do):
-        q, k, v, lam, o, o2, lse = ctx.saved_tensors
-        dq, dk, dv, dlam = fa.diff_backward(q, k, v, lam, o, o2, lse, _strided_ready(do), causal=ctx.causal,
-                                            scale=ctx.scale, deterministic=ctx.deterministic)
-        return dq, dk, dv, dlam, None, None, None
-
-
-class RotaryFunction(torch.autograd.Function):
-    """Rotary positions on q and k; the gradient is the rotation back."""
-
-    @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, sections, interleaved: bool):
-        ctx.save_for_backward(positions, inv_freq)
-        ctx.sections, ctx.interleaved = sections, interleaved
-        k = _strided_ready(k) if k is not None else None
-        return fa.rotary(_strided_ready(q), k, positions, inv_freq, sections, interleaved=interleaved)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, gq, gk):
-        positions, inv_freq = ctx.saved_tensors
-        gk = _strided_ready(gk) if gk is not None else None
-        gq, gk = fa.rotary(_strided_ready(gq), gk, positions, inv_freq, ctx.sections, interleaved=ctx.interleaved,
-                           inverse=True)
-        return gq, gk, None, None, None, None
-
-
 def diff_attn_func(q, k, v, lam, causal: bool = False, softmax_scale=None, deterministic: bool = False):
-    """O = (softmax(scale q_1 k_1^T) - lam softmax(scale q_2 k_2^T)) v, differentiable in q, k, v and lam.
+    """O = (softmax(scale q_1 k_1^T) - lam softmax(scale q_2 k_2^T)) v, differentiable (once) in q, k, v and lam.
     q [B, Sq, H, 2, D], k [B, Sk, Hk, 2, D], v [B, Sk, Hk, Dv]; lam broadcasts to [B, Sq, H]; see ``fa.diff_forward``.
-    ``deterministic=True`` makes the backward's dq bit-reproducible."""
+    The pass saves q, k, v, lam, O, O_2 and both logsumexps. ``deterministic=True`` makes the backward's dq
+    bit-reproducible."""
     scale = q.shape[-1] ** -0.5 if softmax_scale is None else float(softmax_scale)
-    return DiffAttentionFunction.apply(q, k, v, lam, bool(causal), scale, bool(deterministic))
+    return fa.native().diff_attention(q, k, v, lam, causal, scale, deterministic)
 
 
 def rotary_func(q, k, positions, inv_freq, sections=None, interleaved: bool = False):
-    """(q, k) with rotary positions of one or more axes applied, differentiable in q and k (k may be None);
+    """(q, k) with rotary positions of one or more axes applied, differentiable (once) in q and k (k may be None);
     see ``fa.rotary``."""
-    return RotaryFunction.apply(q, k, positions, inv_freq, None if sections is None else tuple(sections),
-                                bool(interleaved))
+    return fa.native().rotary_attached(q, k, positions, inv_freq, sections, interleaved)

@@ -1,4 +1,6 @@
-"""Build libfa.so (the CUDA library) in-tree with nvcc for sm_100a.
+"""Build libfa.so (the CUDA library) in-tree with nvcc for sm_100a, and
+_fa_torch.so (the torch side of differential attention and rotary positions,
+host code only) with the C++ compiler against the installed torch.
 
 Usage: ``python -m exact_io_aware_96_b200.build`` (or ``__graft_entry__.build()``).
 The CUDA runtime is linked statically; the driver API is reached through
@@ -30,9 +32,37 @@ def nvcc() -> str:
 LIB_CHECK = os.path.join(HERE, "libfa_check.so")
 
 
+TORCH_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
+TORCH_LIB = os.path.join(HERE, "_fa_torch.so")
+
+
+def build_torch() -> str:
+    """Build _fa_torch.so, unless it is newer than its sources."""
+    import sysconfig
+
+    import torch
+    sources = [TORCH_SOURCE, os.path.join(INCLUDE, "fa.h"), torch.__file__]
+    if os.path.exists(TORCH_LIB) and all(os.path.getmtime(TORCH_LIB) > os.path.getmtime(s) for s in sources):
+        return TORCH_LIB
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [shutil.which("g++") or "g++", "-shared", "-fPIC", "-O2", "-std=c++17",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *("-I" + d for d in (INCLUDE, os.path.join(at, "include"),
+                                os.path.join(at, "include", "torch", "csrc", "api", "include"),
+                                sysconfig.get_paths()["include"], cuda)),
+           "-o", TORCH_LIB + ".tmp", TORCH_SOURCE, "-L" + os.path.join(at, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("the C++ compiler failed:\n" + res.stdout + res.stderr)
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(verbose: bool = False, extra: list[str] | None = None, check: bool = False) -> str:
-    """Build libfa.so, or with check=True libfa_check.so: the same sources
-    compiled with FA_CHECK=1 (device-side index and bounds checks)."""
+    """Build libfa.so (and _fa_torch.so), or with check=True libfa_check.so: the
+    same sources compiled with FA_CHECK=1 (device-side index and bounds checks)."""
     out = LIB_CHECK if check else LIB
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-shared",
            "-I" + INCLUDE, "-I" + CSRC, "-o", out + ".tmp", *(["-DFA_CHECK=1"] if check else []), *SOURCES]
@@ -46,6 +76,8 @@ def build(verbose: bool = False, extra: list[str] | None = None, check: bool = F
     os.replace(out + ".tmp", out)
     if verbose:
         sys.stdout.write(res.stdout + res.stderr)
+    if not check:
+        build_torch()
     return out
 
 

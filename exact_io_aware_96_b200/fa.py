@@ -12,7 +12,6 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-import struct
 
 import torch
 
@@ -125,10 +124,9 @@ def use_library(path: str) -> None:
     """Route every call of this module through the library at `path` from now
     on (LIB_PATH, or LIB_CHECK_PATH for the check build). The library is
     loaded at the next call."""
-    global _lib, LIB_PATH
+    global _lib, LIB_PATH, _native_module
     LIB_PATH = path
-    _lib = None
-    _packed_fns.clear()
+    _lib = _native_module = None
 
 
 def lib():
@@ -185,17 +183,25 @@ def lib():
     return _lib
 
 
-_packed_fns = {}
+_native_module = None
 
 
-def _packed(name: str):
-    """The entry point `name` taking its params struct as packed bytes."""
-    f = _packed_fns.get(name)
-    if f is None:
-        f = lib()[name]  # a function object of its own
-        f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
-        _packed_fns[name] = f
-    return f
+def native():
+    """The compiled torch side of differential attention and rotary positions
+    (csrc/fa_torch.cpp), calling the library that is loaded. Raises if it has
+    not been built."""
+    global _native_module
+    if _native_module is None:
+        L = lib()
+        try:
+            from . import _fa_torch as m
+        except ImportError as e:
+            raise RuntimeError("_fa_torch.so is missing: build it with `python -m exact_io_aware_96_b200.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.fa_diff_fwd, L.fa_diff_bwd, L.fa_rotary, L.fa_diff_fwd_workspace_size,
+                           L.fa_diff_bwd_workspace_size, L.fa_strerror)))
+        _native_module = m
+    return _native_module
 
 
 # ---------------------------------------------------------------- raw C ABI
@@ -507,19 +513,8 @@ def backward(q, k, v, o, lse, do, causal=False, scale=None, dq=None, dk=None, dv
 
 
 # ------------------------------------- differential attention, rotary positions
-# These helpers are called on single tokens, where the GPU's part is a few
-# microseconds, so they spend little on the host: parameter structs are packed
-# in one step (the layouts of DiffFwdParams, DiffBwdParams and RotaryParams;
-# "@" pads as the C compiler does), tensors are asked for their shape and
-# strides once, and the detailed checks run only where a quick one fails.
-_T = "Pqqq"  # fa_tensor
-_LAM = "Pqqqiiii"  # fa_diff_lambda
-_DIFF_FWD = struct.Struct("@" + 5 * _T + _LAM + "P" + 2 * _T + "P7ifiiPN")
-_DIFF_BWD = struct.Struct("@" + 8 * _T + "P" + _LAM + 5 * _T + "P7ifiiPNi0P")
-_ROTARY = struct.Struct("@" + 4 * _T + f"PqqqiPii{FA_ROTARY_MAX_AXES}i8i0P")
-_NO_TENSOR = (0, 0, 0, 0)
-
-
+# These are called on single tokens, where the GPU's part is a few microseconds:
+# checks, allocations and parameter structs are compiled (native()).
 @contextlib.contextmanager
 def _on(dev, stream):
     """Makes `dev` current, and the caller's stream (if any) torch's current
@@ -537,83 +532,9 @@ def _on(dev, stream):
             yield
 
 
-def _elsewhere(dev, stream) -> bool:
+def _elsewhere(t: torch.Tensor, stream) -> bool:
     """Whether a call has to change the current device or stream first."""
-    if dev.type != "cuda":
-        raise ValueError("tensors must live on a CUDA device (the library has no CPU path)")
-    return stream is not None or dev.index != torch.cuda.current_device()
-
-
-try:  # the handle alone, without a Stream object around it
-    _raw_stream = torch._C._cuda_getCurrentRawStream
-except AttributeError:  # a torch without CUDA, or without this function
-    def _raw_stream(index: int) -> int:
-        return torch.cuda.current_stream(index).cuda_stream
-
-
-def _flat(name: str, t: torch.Tensor):
-    """fa_tensor of a [B, S, H, D] view."""
-    sb, ss, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    return t.data_ptr(), sb, ss, sh
-
-
-def _pair(name: str, t: torch.Tensor):
-    """The two maps' fa_tensors of a [B, S, H, 2, D] view of 16-bit values."""
-    sb, ss, sh, sc, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    at = t.data_ptr()
-    return at, sb, ss, sh, at + 2 * sc, sb, ss, sh
-
-
-def _need(name: str, t: torch.Tensor, shape, dtype, dev) -> None:
-    if t.shape != shape or t.dtype is not dtype or t.device != dev:
-        _expect(name, t, shape, dtype, dev)
-
-
-def _diff_dims(q, k, v):
-    if q.dim() != 5 or k.dim() != 5 or v.dim() != 4 or q.shape[3] != 2 or k.shape[3] != 2:
-        raise ValueError("expected q [B, Sq, H, 2, D], k [B, Sk, Hk, 2, D] and v [B, Sk, Hk, Dv]")
-    B, Sq, H, _, D = q.shape
-    _, Sk, Hk, Dv = v.shape
-    dt, dev = _dtype_code(q), q.device
-    _need("k", k, (B, Sk, Hk, 2, D), q.dtype, dev)
-    _need("v", v, (B, Sk, Hk, Dv), q.dtype, dev)
-    if Hk < 1 or H % Hk:
-        raise ValueError(f"{H} query heads cannot share {Hk} key heads evenly")
-    return B, Sq, H, D, Sk, Hk, Dv, dt, dev
-
-
-def _lambda(lam, B, Sq, H, dtype, dev):
-    if not isinstance(lam, torch.Tensor) or lam.dim() > 3:
-        raise ValueError("lam must be a tensor that broadcasts to [B, Sq, H]")
-    none = 3 - lam.dim()
-    eb, es, eh = (1,) * none + tuple(lam.shape)
-    if (eb != 1 and eb != B) or (es != 1 and es != Sq) or (eh != 1 and eh != H):
-        raise ValueError(f"lam: {tuple(lam.shape)} does not broadcast to [{B}, {Sq}, {H}]")
-    if lam.dtype is not torch.float32 and lam.dtype is not dtype:
-        raise TypeError(f"lam: expected float32 or {dtype}, got {lam.dtype}")
-    if lam.device != dev:
-        raise ValueError(f"lam is on {lam.device}, q on {dev}")
-    code = FA_LAMBDA_FP32 if lam.dtype is torch.float32 else _DT[lam.dtype]
-    return (lam.data_ptr(), *((0,) * none + lam.stride()), eb, es, eh, code)
-
-
-def _diff_lse(lse, B, H, Sq, dev):
-    _need("lse", lse, (2, B, H, Sq), torch.float32, dev)
-    if not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 [2, B, H, Sq] tensor")
-
-
-def _ws(workspace, dev):
-    """(address, bytes) of a workspace, or of none."""
-    if workspace is None:
-        return 0, 0
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous buffer on {dev}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return t.is_cuda and (stream is not None or t.get_device() != torch.cuda.current_device())
 
 
 def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=False, out=None, out2=None, lse=None,
@@ -627,37 +548,10 @@ def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=Fa
     entry b attends to its first k_lens[b] keys, and the causal mask aligns to
     that end. LSE is fp32 [2, B, H, Sq]. O2 = softmax(scale q_2 k_2^T) v is
     written if need_o2 or out2 asks for it (diff_backward needs it), else None."""
-    B, Sq, H, D, Sk, Hk, Dv, dt, dev = _diff_dims(q, k, v)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if _elsewhere(q, stream):
+        with _on(q.device, stream):
             return diff_forward(q, k, v, lam, causal, scale, k_lens, need_o2, out, out2, lse, workspace)
-    lp = _lambda(lam, B, Sq, H, q.dtype, dev)
-    if k_lens is not None:
-        _need("k_lens", k_lens, (B,), torch.int32, dev)
-        if not k_lens.is_contiguous():
-            raise ValueError("k_lens must be contiguous")
-    shape, causal = (B, Sq, H, Dv), 1 if causal else 0
-    if out is None:
-        out = q.new_empty(shape)
-    else:
-        _need("out", out, shape, q.dtype, dev)
-    if out2 is not None:
-        _need("out2", out2, shape, q.dtype, dev)
-    elif need_o2:
-        out2 = q.new_empty(shape)
-    if lse is None:
-        lse = torch.empty((2, B, H, Sq), dtype=torch.float32, device=dev)
-    else:
-        _diff_lse(lse, B, H, Sq, dev)
-    if workspace is None and Sq <= 16:  # calls of more rows need none
-        n = fa_diff_fwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    p = _DIFF_FWD.pack(*_pair("q", q), *_pair("k", k), *_flat("v", v), *lp,
-                       0 if k_lens is None else k_lens.data_ptr(), *_flat("out", out),
-                       *(_NO_TENSOR if out2 is None else _flat("out2", out2)), lse.data_ptr(),
-                       B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale), causal, dt,
-                       *_ws(workspace, dev))
-    st = _packed("fa_diff_fwd")(p, _raw_stream(dev.index))
+    st, out, lse, out2 = native().diff_forward(q, k, v, lam, causal, scale, k_lens, need_o2, out, out2, lse, workspace)
     if st != FA_OK:
         raise FaError(st, "fa_diff_fwd")
     return out, lse, out2
@@ -669,35 +563,12 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=Non
     and lse it takes. dLam has lam's shape and dtype: the gradient is summed
     over the axes lam is broadcast over. ``deterministic=True`` sums dQ in a
     fixed order (dK, dV and dLam always are)."""
-    B, Sq, H, D, Sk, Hk, Dv, dt, dev = _diff_dims(q, k, v)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if _elsewhere(q, stream):
+        with _on(q.device, stream):
             return diff_backward(q, k, v, lam, o, o2, lse, do, causal, scale, dq, dk, dv, dlam, workspace, None,
                                  deterministic)
-    lp = _lambda(lam, B, Sq, H, q.dtype, dev)
-    shape, det = (B, Sq, H, Dv), 1 if deterministic else 0
-    for name, t in (("o", o), ("o2", o2), ("do", do)):
-        _need(name, t, shape, q.dtype, dev)
-    _diff_lse(lse, B, H, Sq, dev)
-    grads = []
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dlam", dlam, lam)):
-        if t is None:
-            t = like.new_empty(like.shape)
-        else:
-            _need(name, t, like.shape, like.dtype, dev)
-        grads.append(t)
-    dq, dk, dv, dlam = grads
-    if not dlam.is_contiguous():
-        raise ValueError("dlam must be contiguous")
-    causal = 1 if causal else 0
-    if workspace is None:
-        n = fa_diff_bwd_workspace_size(B, H, Hk, Sq, Sk, D, Dv, causal, det)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    p = _DIFF_BWD.pack(*_pair("q", q), *_pair("k", k), *_flat("v", v), *_flat("o", o), *_flat("o2", o2),
-                       *_flat("do", do), lse.data_ptr(), *lp, *_pair("dq", dq), *_pair("dk", dk), *_flat("dv", dv),
-                       dlam.data_ptr(), B, H, Hk, Sq, Sk, D, Dv, D ** -0.5 if scale is None else float(scale),
-                       causal, dt, *_ws(workspace, dev), det)
-    st = _packed("fa_diff_bwd")(p, _raw_stream(dev.index))
+    st, dq, dk, dv, dlam = native().diff_backward(q, k, v, lam, o, o2, lse, do, causal, scale, dq, dk, dv, dlam,
+                                                  workspace, deterministic)
     if st != FA_OK:
         raise FaError(st, "fa_diff_bwd")
     return dq, dk, dv, dlam
@@ -709,20 +580,6 @@ def rotary_inv_freq(sections, base=10000.0, per_axis=False, device="cuda") -> to
     counts = list(sections) if per_axis else [sum(sections)]
     return torch.tensor([float(base) ** (-j / n) for n in counts for j in range(n)], dtype=torch.float64,
                         device=device)
-
-
-def _heads(name: str, t: torch.Tensor, B, S, D, dtype, dev):
-    """(heads, fa_tensor) of [B, S, heads, D], or of [B, S, H, 2, D] with the two maps as neighbouring heads."""
-    if t.dim() == 5:
-        try:
-            t = t.view(t.shape[0], t.shape[1], -1, t.shape[4])
-        except RuntimeError:
-            raise ValueError(f"{name}: the head axes of [B, S, H, 2, D] must be one run of heads") from None
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [B, S, heads, D] or [B, S, H, 2, D]")
-    n = t.shape[2]
-    _need(name, t, (B, S, n, D), dtype, dev)
-    return n, _flat(name, t)
 
 
 def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
@@ -737,55 +594,10 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
     all on the only axis). Pairs are columns (j, j + R), or (2j, 2j + 1) if
     interleaved; columns from 2R on are copied. inverse turns back: it is also
     the gradient. out_q may be q and out_k may be k (in place)."""
-    dt, dev, dtype = _dtype_code(q), q.device, q.dtype
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if _elsewhere(q, stream):
+        with _on(q.device, stream):
             return rotary(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k)
-    B, S, D = q.shape[0], q.shape[1], q.shape[-1]
-    H, vq = _heads("q", q, B, S, D, dtype, dev)
-    Hk, vk = _heads("k", k, B, S, D, dtype, dev) if k is not None else (0, _NO_TENSOR)
-    if positions.dim() == 2:
-        positions = positions[None]
-    if positions.dim() != 3 or positions.shape[1:] != (B, S):
-        raise ValueError(f"positions: expected [axes, {B}, {S}], got {tuple(positions.shape)}")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"positions: expected int32 or int64, got {positions.dtype}")
-    if inv_freq.dtype not in (torch.float32, torch.float64):
-        raise TypeError(f"inv_freq: expected float32 or float64, got {inv_freq.dtype}")
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous [pairs] tensor")
-    for name, t in (("positions", positions), ("inv_freq", inv_freq)):
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, q on {dev}")
-    axes, pairs = positions.shape[0], inv_freq.shape[0]
-    sections = (pairs,) if sections is None else tuple(sections)
-    if len(sections) != axes or not 1 <= axes <= FA_ROTARY_MAX_AXES:
-        raise ValueError(f"sections: expected one entry for each of 1 to {FA_ROTARY_MAX_AXES} axes, got "
-                         f"{len(sections)} for {axes}")
-    if sum(sections) != pairs or min(sections) < 0:
-        raise ValueError(f"sections {sections} do not add up to inv_freq's {pairs} pairs")
-    if 2 * pairs > D:
-        raise ValueError(f"{pairs} pairs do not fit into {D} columns")
-    if out_q is None:
-        out_q = q.new_empty(q.shape)
-    elif out_q.shape != q.shape:
-        _expect("out_q", out_q, q.shape, dtype, dev)
-    if k is None:
-        if out_k is not None:
-            raise ValueError("out_k without k")
-        wk = _NO_TENSOR
-    else:
-        if out_k is None:
-            out_k = k.new_empty(k.shape)
-        elif out_k.shape != k.shape:
-            _expect("out_k", out_k, k.shape, dtype, dev)
-        wk = _heads("out_k", out_k, B, S, D, dtype, dev)[1]
-    p = _ROTARY.pack(*vq, *vk, *_heads("out_q", out_q, B, S, D, dtype, dev)[1], *wk, positions.data_ptr(),
-                     *positions.stride(), 1 if positions.dtype is torch.int64 else 0, inv_freq.data_ptr(),
-                     1 if inv_freq.dtype is torch.float64 else 0, axes,
-                     *sections, *(0,) * (FA_ROTARY_MAX_AXES - axes), B, S, H, Hk, D,
-                     1 if interleaved else 0, 1 if inverse else 0, dt)
-    st = _packed("fa_rotary")(p, _raw_stream(dev.index))
+    st, out_q, out_k = native().rotary(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k)
     if st != FA_OK:
         raise FaError(st, "fa_rotary")
     return out_q, out_k

@@ -1,5 +1,4 @@
-"""Differential attention and rotary positions without a GPU: struct layouts,
-workspace sizes, refusals (all on the host, before any CUDA call), the oracle."""
+"""Differential attention and rotary positions without a GPU: workspace sizes, refusals (all on the host, before any CUDA call), the oracle."""
 import ctypes
 
 import numpy as np
@@ -10,42 +9,6 @@ from exact_io_aware_96_b200 import fa
 from oracle.differential import differential, rotary
 
 A = 0x10000  # an aligned fake address: validation fails before any use
-
-
-def leaves(s):
-    """Every scalar of a ctypes struct, in order, set to 1, 2, 3, ..."""
-    n = 0
-
-    def fill(x, cls):
-        nonlocal n
-        for name, t in cls._fields_:
-            if issubclass(t, ctypes.Structure):
-                fill(getattr(x, name), t)
-            elif issubclass(t, ctypes.Array):
-                arr = getattr(x, name)
-                for i in range(len(arr)):
-                    if issubclass(t._type_, ctypes.Structure):
-                        fill(arr[i], t._type_)
-                    else:
-                        n += 1
-                        arr[i] = n
-            else:
-                n += 1
-                setattr(x, name, n)
-    fill(s, type(s))
-    return n
-
-
-@pytest.mark.parametrize("packed,cls", [(fa._DIFF_FWD, fa.DiffFwdParams), (fa._DIFF_BWD, fa.DiffBwdParams),
-                                        (fa._ROTARY, fa.RotaryParams)])
-def test_packed_layouts_are_the_structs(packed, cls):
-    s = cls()
-    n = leaves(s)
-    assert packed.size == ctypes.sizeof(cls)
-    back = cls.from_buffer_copy(packed.pack(*range(1, n + 1)))
-    other = cls()
-    leaves(other)
-    assert packed.unpack(bytes(back)) == packed.unpack(bytes(other)) == tuple(range(1, n + 1))
 
 
 def tens(S=128, H=2, D=64, at=A):
@@ -160,6 +123,22 @@ def test_cpu_tensors_are_refused(fa_lib):
         fa.diff_forward(q.float(), k.float(), v.float(), torch.ones(2))
     with pytest.raises(ValueError, match="expected q"):
         fa.diff_forward(v, k, v, torch.ones(2))
+
+
+def test_helpers_check_their_tensors(fa_lib):
+    """Shapes and dtypes, found before any CUDA call."""
+    half = lambda *s: torch.zeros(s).half()  # noqa: E731
+    q, k, v, lam = half(1, 4, 2, 2, 64), half(1, 6, 2, 2, 64), half(1, 6, 2, 128), torch.ones(2)
+    for bad, error in (((q, half(1, 6, 2, 2, 32), v, lam), ValueError), ((q, k, half(1, 5, 2, 128), lam), ValueError),
+                       ((q, k.bfloat16(), v, lam), TypeError), ((q, half(1, 6, 3, 2, 64), half(1, 6, 3, 128), lam), ValueError),
+                       ((q, k, v, 0.5), TypeError)):
+        with pytest.raises(error):
+            fa.diff_forward(*bad)
+    x, pos, f = half(1, 4, 2, 64), torch.zeros(3, 1, 4, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.rotary(x, None, pos, f, (8, 12, 12))
+    with pytest.raises(TypeError, match="fp16/bf16"):
+        fa.rotary(x.float(), None, pos, f, (8, 12, 12))
 
 
 def test_oracle_gradients_are_its_differences():

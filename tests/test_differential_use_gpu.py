@@ -314,6 +314,37 @@ def test_first_call_inside_a_capture(fa_lib, Sq):
     assert "captured first" in out.stdout, out.stderr[-1500:]
 
 
+def test_refusals_on_the_device(fa_lib):
+    q, k, v, lam, _ = (x.cuda() for x in case(1, 8, 12, 4, 2, 64, 128, torch.float16, 53))
+    pos, f = torch.zeros((3, 1, 8), dtype=torch.int32, device="cuda"), fa.rotary_inv_freq(SECTIONS)
+    x = q.flatten(2, 3)
+    for call, error in (
+            (lambda: fa.diff_forward(q, k, v, lam[:, :3]), ValueError),
+            (lambda: fa.diff_forward(q, k, v, lam.bfloat16()), TypeError),
+            (lambda: fa.diff_forward(q, k, v, lam.cpu()), ValueError),
+            (lambda: fa.diff_forward(q, k, v.cpu(), lam), ValueError),
+            (lambda: fa.diff_forward(q, k, v, lam, k_lens=torch.ones(1, device="cuda")), TypeError),
+            (lambda: fa.diff_forward(q, k, v, lam, k_lens=torch.ones(2, dtype=torch.int32, device="cuda")), ValueError),
+            (lambda: fa.diff_forward(q, k, v, lam, out=v), ValueError),
+            (lambda: fa.diff_forward(q, k, v, lam, scale=-1.0), fa.FaError),
+            (lambda: fa.diff_forward(q[:, :1].expand(1, 8, 4, 2, 64), k, v, lam), fa.FaError),
+            (lambda: fa.diff_forward(q[:0], k[:0], v[:0], lam[:0]), fa.FaError),
+            (lambda: fa.diff_forward(q[:, :1], k, v, lam[:, :1], workspace=torch.empty(0, dtype=torch.uint8)), ValueError),
+            (lambda: fa.diff_forward(q[..., :4], k[..., :4], v, lam), fa.FaError),
+            (lambda: fa.rotary(x, None, pos, f, (8, 12)), ValueError),
+            (lambda: fa.rotary(x, None, pos, f, (8, 12, 11)), ValueError),
+            (lambda: fa.rotary(x, None, pos, f, (40, -20, 12)), ValueError),
+            (lambda: fa.rotary(x, None, pos.float(), f, SECTIONS), TypeError),
+            (lambda: fa.rotary(x, None, pos[:, :, :7], f, SECTIONS), ValueError),
+            (lambda: fa.rotary(x[..., :32], None, pos, f, SECTIONS), ValueError),
+            (lambda: fa.rotary(x, None, pos, f.half(), SECTIONS), TypeError),
+            (lambda: fa.rotary(x, None, pos, f.cpu(), SECTIONS), ValueError),
+            (lambda: fa.rotary(x, None, pos, f, SECTIONS, out_k=x), ValueError)):
+        with pytest.raises(error):
+            call()
+    status_clear()
+
+
 def test_no_second_derivative(fa_lib):
     q, k, v, lam, _ = (x.cuda() for x in case(1, 8, 8, 1, 1, 64, 64, torch.float16, 23))
     q.requires_grad_()
