@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a) {
   const int items = nt * a.per_tok;
   Pack va[U], vb[U];
   uint16_t* out[U];
-  int c0[U];  // first (cos, sin) of a rotated group; -1: copied; -2: none
+  int c0[U];    // first (cos, sin) of a rotated group; -1: copied; -2: none
+  int left[U];  // INTER: the head's pairs from there on
   auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a) {
       const uint16_t* x = a.x[w] + b * a.xs[w][0] + s * a.xs[w][1] + h * a.xs[w][2] + col;
       out[u] = a.y[w] + b * a.ys[w][0] + s * a.ys[w][1] + h * a.ys[w][2] + col;
       c0[u] = rot ? t * a.R + (INTER ? it * (VEC / 2) : it * VEC) : -1;
+      left[u] = a.R - it * (VEC / 2);
       va[u] = *reinterpret_cast<const Pack*>(x);
       if (!INTER && rot) vb[u] = *reinterpret_cast<const Pack*>(x + a.R);
     }
@@ -140,10 +142,9 @@ __global__ void __launch_bounds__(256) fa_rotary_kernel(const RotArgs a) {
       if (c0[u] >= 0) {
         const float2* c = cs + c0[u];
         if constexpr (INTER) {
-          const int left = a.R - c0[u] % a.R;  // pairs of this head from here on
 #pragma unroll
           for (int e = 0; e < VEC / 2; ++e)
-            if (e < left) {
+            if (e < left[u]) {
               const float2 q = c[e], x = unpack2<BF16>(va[u].w[e]);
               va[u].w[e] = pack2<BF16>(x.x * q.x - x.y * q.y, x.x * q.y + x.y * q.x);
             }
