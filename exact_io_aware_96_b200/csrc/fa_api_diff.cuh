@@ -115,8 +115,13 @@ int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
 // The few-row form (fa_diff_rows.cuh): whether a call takes it, and its teams.
 // Two CTAs run on an SM. Where a team of one CTA per (key head, row tile) is
 // small, as many teams as fit at once share the keys evenly; large teams get a
-// few waves, which even out by themselves. Many batch entries, or caches of two
-// units per stream at most, go direct: no second kernel.
+// few waves, which even out by themselves. "Direct" saves the second kernel and
+// the restart between batch entries (about 8 and 4 us), but leaves an entry's
+// keys to one CTA, which takes 18 ns a key alone and 28 on a full GPU; it is
+// taken where that is estimated 15% shorter, and for caches of two units per
+// stream at most. Measured, us, direct against teams (D = 64, DV = 128): 32
+// entries x 8 heads x 500 keys 16.7 / 21.7; 8 x 8 x 1000 22.5 / 15.8; 1 x 8 x
+// 1000 22.0 / 8.2.
 struct RowsPlan {
   bool rows = false;  // false: the tiled kernel
   int teams = 0;      // 0: direct
@@ -129,8 +134,13 @@ RowsPlan rows_plan(int B, int H, int Hk, int Sq, int Sk, int Dv) {
   const int64_t slots = 2 * int64_t(std::max(1, sm_count())), team = int64_t(Hk) * ((R + 15) / 16);
   if (team * B > (int64_t(1) << 31) - 1) return p;
   p.rows = true;
-  if (Sk <= 256 || team * B >= 4 * slots) return p;
+  const int64_t items = team * B;
   const int64_t teams = team * 4 <= slots ? slots / team : (4 * slots + team - 1) / team;
+  const double full = std::min(1.0, double(items) / double(slots)), waves = double((items + slots - 1) / slots);
+  const double direct_us = waves * (4 + Sk * std::max(0.018, 0.028 * full));
+  const double teams_us =
+      8 + (2 * int64_t(B) > teams ? 4 : 0) + double(items) * Sk * (128 + (Dv <= 64 ? 64 : 128)) * 2 / 5.4e6;
+  if (Sk <= 256 || items >= 4 * slots || 1.15 * direct_us < teams_us) return p;
   p.teams = int(std::min<int64_t>(teams, (int64_t(B) * ((int64_t(Sk) + 63) / 64) + 1) / 2));
   const uint64_t parts = uint64_t(B + p.teams) * Hk * R * 2;
   p.off_o = round256(parts * sizeof(float2));
