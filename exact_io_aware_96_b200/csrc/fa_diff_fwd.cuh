@@ -156,7 +156,14 @@ __global__ void __launch_bounds__(576, 1)
   const int n = fwd_kv_blocks(q0, a.Sq, sk, a.causal);
   checked(q0 < a.Sq && b < a.B && hk < a.Hk, 401);
 
-  if (threadIdx.x == 0) {
+  // The loader's thread sets the barriers up itself and asks for Q and the
+  // first keys at once, while the MMA warp allocates tensor memory.
+  if (warp == L::kLoaderWarp && lane == 0) {
+    prefetch_tmap(&tmQ1);
+    prefetch_tmap(&tmQ2);
+    prefetch_tmap(&tmK1);
+    prefetch_tmap(&tmK2);
+    prefetch_tmap(&tmV);
     mbar_init(q_full, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(&k_full[s], 1);
@@ -174,13 +181,14 @@ __global__ void __launch_bounds__(576, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-  }
-  if (warp == L::kLoaderWarp && lane == 0) {
-    prefetch_tmap(&tmQ1);
-    prefetch_tmap(&tmQ2);
-    prefetch_tmap(&tmK1);
-    prefetch_tmap(&tmK2);
-    prefetch_tmap(&tmV);
+    if (n > 0) {
+      mbar_arrive_expect_tx(q_full, 2 * L::BLK);
+      tma_load_4d(smem + L::OFF_Q, &tmQ1, q_full, 0, q0, h, b);
+      tma_load_4d(smem + L::OFF_Q + L::BLK, &tmQ2, q_full, 0, q0, h, b);
+      mbar_arrive_expect_tx(&k_full[0], 2 * L::BLK);
+      tma_load_4d(smem + L::OFF_K, &tmK1, &k_full[0], 0, 0, hk, b);
+      tma_load_4d(smem + L::OFF_K + L::BLK, &tmK2, &k_full[0], 0, 0, hk, b);
+    }
   }
   if (warp == L::kMmaWarp) {
     tmem_alloc(tmem_slot, L::TMEM_COLS);
@@ -194,17 +202,16 @@ __global__ void __launch_bounds__(576, 1)
   if (warp == L::kLoaderWarp) {
     // ------------------------------------------------------------ loader
     if (lane == 0 && n > 0) {
-      mbar_arrive_expect_tx(q_full, 2 * L::BLK);
-      tma_load_4d(smem + L::OFF_Q, &tmQ1, q_full, 0, q0, h, b);
-      tma_load_4d(smem + L::OFF_Q + L::BLK, &tmQ2, q_full, 0, q0, h, b);
       int nk = 0, nv = 0;  // loads issued
       for (int j = 0; j < n; ++j) {
         const int ks = j % KS, vs = j % VS;
         checked(j * 128 < sk, 402);
-        if (!wait_bar(&k_empty[ks], ((j / KS) & 1) ^ 1, abort_flag, kRoleLoader, j)) break;
-        mbar_arrive_expect_tx(&k_full[ks], 2 * L::BLK);
-        tma_load_4d(smem + L::OFF_K + ks * 2 * L::BLK, &tmK1, &k_full[ks], 0, j * 128, hk, b);
-        tma_load_4d(smem + L::OFF_K + (ks * 2 + 1) * L::BLK, &tmK2, &k_full[ks], 0, j * 128, hk, b);
+        if (j > 0) {
+          if (!wait_bar(&k_empty[ks], ((j / KS) & 1) ^ 1, abort_flag, kRoleLoader, j)) break;
+          mbar_arrive_expect_tx(&k_full[ks], 2 * L::BLK);
+          tma_load_4d(smem + L::OFF_K + ks * 2 * L::BLK, &tmK1, &k_full[ks], 0, j * 128, hk, b);
+          tma_load_4d(smem + L::OFF_K + (ks * 2 + 1) * L::BLK, &tmK2, &k_full[ks], 0, j * 128, hk, b);
+        }
         ++nk;
         if (!wait_bar(&v_empty[vs], ((j / VS) & 1) ^ 1, abort_flag, kRoleLoader, j)) break;
         mbar_arrive_expect_tx(&v_full[vs], L::VB * L::BLK);
@@ -422,6 +429,10 @@ __global__ void __launch_bounds__(576, 1)
     // writes a quarter of the columns from both accumulators.
     lsum[(t * 2 + c) * 128 + r] = l;
     if (c == 0) msm[t * 128 + r] = m;
+    const bool valid = row < a.Sq;
+    const bool has = sk > 0 && (!a.causal || row + off >= 0);  // some key is allowed (the same in both maps)
+    const float lam = valid && has ? load_lam(a.lam, a.lam_kind, b * a.lam_s[0] + row * a.lam_s[1] + h * a.lam_s[2])
+                                   : 0.f;  // asked for here: it arrives while the warps meet
     constexpr int kAllBar = 9;
     bool go = named_bar_and(kAllBar, 512, ok && !*abort_flag);
     const int wg = warp >> 2;
@@ -433,12 +444,8 @@ __global__ void __launch_bounds__(576, 1)
       tc_fence_after();
     }
     if (go) {
-      const bool valid = row < a.Sq;
       const float l1 = lsum[r] + lsum[128 + r], l2 = lsum[256 + r] + lsum[384 + r];
       const float m1 = msm[r], m2 = msm[128 + r];
-      const bool has = sk > 0 && (!a.causal || row + off >= 0);  // some key is allowed (the same in both maps)
-      const float lam = valid && has ? load_lam(a.lam, a.lam_kind, b * a.lam_s[0] + row * a.lam_s[1] + h * a.lam_s[2])
-                                     : 0.f;
       const float inv1 = has ? 1.f / l1 : 0.f, inv2 = has ? 1.f / l2 : 0.f;
       uint32_t o1[NC], o2[NC];
       if (n > 0) {
@@ -457,27 +464,56 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
         for (int i = 0; i < NC; ++i) o1[i] = o2[i] = 0u;
       }
-      if (valid && checked(b < a.B && h < a.H && row < a.Sq, 403)) {
-        uint16_t* orow = reinterpret_cast<uint16_t*>(a.o) + b * a.o_s[0] + row * a.o_s[1] + h * a.o_s[2] + cb;
-        uint16_t* orow2 = reinterpret_cast<uint16_t*>(a.o2) + b * a.o2_s[0] + row * a.o2_s[1] + h * a.o2_s[2] + cb;
+      // A row's quarter goes through shared memory (Q's, read for the last time
+      // above; 16-byte chunks swizzled so that neither side meets a bank
+      // conflict): straight from the registers a warp's store would touch 32
+      // rows' lines at 16 bytes each, from here it writes 8 rows of 64 bytes.
+      constexpr int CH = NC / 8, RPI = 32 / CH;  // chunks of a row, rows of one store
+      const int wrow = row - lane;               // the warp's first row
+      uint8_t* stage = smem + L::OFF_Q + warp * 32 * NC * 2;
+      auto slot = [&](int rr, int ch) {
+        return reinterpret_cast<uint4*>(stage + rr * NC * 2 + ((ch ^ (rr / (8 / CH) & (CH - 1))) << 4));
+      };
+      auto store_rows = [&](void* base, const int64_t* st) {
+        uint16_t* ob = reinterpret_cast<uint16_t*>(base) + b * st[0] + h * st[2] + cb;
+        const int ch = lane % CH;
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NC / 8; ++i) {
-          uint32_t w[4], w2[4];
+        for (int i = 0; i < CH; ++i) {
+          const int rr = i * RPI + lane / CH, gr = wrow + rr;
+          const uint4 w = *slot(rr, ch);
+          if (gr < a.Sq && cb + 8 * ch < a.dv && checked(b < a.B && h < a.H, 403))
+            *reinterpret_cast<uint4*>(ob + gr * st[1] + 8 * ch) = w;
+        }
+        __syncwarp();
+      };
+      if (a.o2 != nullptr) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int x = 8 * i + 2 * e;
-            const float y0 = has ? __uint_as_float(o2[x]) * inv2 : 0.f;
-            const float y1 = has ? __uint_as_float(o2[x + 1]) * inv2 : 0.f;
-            const float x0 = has ? __uint_as_float(o1[x]) * inv1 : 0.f;
-            const float x1 = has ? __uint_as_float(o1[x + 1]) * inv1 : 0.f;
-            w[e] = pack2<BF16>(x0 - lam * y0, x1 - lam * y1);
-            w2[e] = pack2<BF16>(y0, y1);
+            w[e] = has ? pack2<BF16>(__uint_as_float(o2[x]) * inv2, __uint_as_float(o2[x + 1]) * inv2) : 0u;
           }
-          if (cb + 8 * i < a.dv) {
-            reinterpret_cast<uint4*>(orow)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (a.o2 != nullptr) reinterpret_cast<uint4*>(orow2)[i] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-          }
+          *slot(lane, i) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        store_rows(a.o2, a.o2_s);
+      }
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = 8 * i + 2 * e;
+          const float x0 = __uint_as_float(o1[x]) * inv1 - lam * (__uint_as_float(o2[x]) * inv2);
+          const float x1 = __uint_as_float(o1[x + 1]) * inv1 - lam * (__uint_as_float(o2[x + 1]) * inv2);
+          w[e] = has ? pack2<BF16>(x0, x1) : 0u;
+        }
+        *slot(lane, i) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      store_rows(a.o, a.o_s);
+      if (valid) {
         if (wg < 2) {  // warpgroup 0 writes map 1's LSE, warpgroup 1 map 2's
           const float lm = wg ? m2 : m1, ll = wg ? l2 : l1;
           a.lse[((static_cast<int64_t>(wg) * a.B + b) * a.H + h) * a.Sq + row] =
