@@ -107,6 +107,8 @@ int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.causal = p->causal;
   a.n_qblocks = (p->Sq + 127) / 128;
+  a.by_order = fa::make_div(p->causal ? p->B * p->H : a.n_qblocks);
+  a.by_H = fa::make_div(p->H), a.by_group = fa::make_div(p->H / p->Hk);
   const unsigned grid = unsigned(int64_t(a.n_qblocks) * p->B * p->H);
   kern<<<grid, L::kThreads, L::SMEM_ALLOC, stream>>>(m[0], m[1], m[2], m[3], m[4], a);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -331,6 +333,10 @@ int launch_diff_bwd(const fa_diff_bwd_params* p, cudaStream_t stream) {
   const fa_diff_lambda& lam = p->lambda;
   if (lam.extent_b == p->B && lam.extent_s == p->Sq && lam.extent_h == p->H) a.dlam = p->dlambda;
   a.parts = w.parts;
+  a.group = p->H / p->Hk;
+  a.by_H = fa::make_div(p->H), a.by_Hk = fa::make_div(p->Hk), a.by_parts = fa::make_div(w.parts);
+  a.by_Sq = fa::make_div(p->Sq), a.by_Sq_pad = fa::make_div(a.Sq_pad), a.by_Sk = fa::make_div(p->Sk);
+  a.by_order = fa::make_div(p->causal ? p->B * p->Hk : a.nkb);
   a.dkv_part = w.parts > 1 ? reinterpret_cast<float*>(ws + w.off_dkv) : nullptr;
   const int64_t rows = int64_t(p->B) * p->H * a.Sq_pad;
   fa::fa_diff_pre<DV, BF16><<<unsigned(rows * (DV / 8) / 256), 256, 0, stream>>>(a);

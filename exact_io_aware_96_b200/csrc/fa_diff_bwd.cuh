@@ -88,10 +88,13 @@ struct DiffBwdArgs {
   float* dq_part;  // deterministic mode: fp32 [B*H][nqb][nkb][2][128][64] slots; else null
   int B, H, Hk, Sq, Sk, Sq_pad;
   int nqb, nkb;    // ceil(Sq / 128), ceil(Sk / 128)
+  int group;       // H / Hk
   int parts;       // CTAs that share a key block's (head, query block) list
   int d, dv_cols;  // head_dim of q and k; columns of v
   float scale, scale_log2;
   int causal;
+  Div by_H, by_Sq, by_Sq_pad, by_Sk, by_Hk, by_parts;
+  Div by_order;  // the faster dimension of the grid order: B x Hk with a causal mask, nkb without
 };
 
 constexpr int kDiffVec = 5 * 64;  // floats of one chunk's row terms
@@ -168,10 +171,9 @@ __global__ void __launch_bounds__(256) fa_diff_pre(const DiffBwdArgs a) {
   const int part = static_cast<int>(gid % G);
   const int64_t nrows = static_cast<int64_t>(a.B) * a.H * a.Sq_pad;
   if (row >= nrows) return;  // whole groups leave together: G divides 32, nrows * G is a multiple of 256
-  const int i = static_cast<int>(row % a.Sq_pad);
-  const int bh = static_cast<int>(row / a.Sq_pad);
-  const int h = bh % a.H;
-  const int b = bh / a.H;
+  int i, h;
+  const int bh = static_cast<int>(quo_rem(row, a.by_Sq_pad, &i));
+  const int b = static_cast<int>(quo_rem(bh, a.by_H, &h));
   float d_o = 0.f, d_2 = 0.f;  // dO . O, dO . O_2
   if (i < a.Sq && part * 8 < a.dv_cols && checked(b < a.B && h < a.H, 501)) {
     auto at = [&](const void* p, const int64_t(&s)[3]) {
@@ -244,10 +246,9 @@ __global__ void __launch_bounds__(256) fa_diff_dq(const DiffBwdArgs a) {
   const int c = blockIdx.y;
   const int64_t bhs = static_cast<int64_t>(a.B) * a.H;
   if (row >= bhs * a.Sq || part * 8 >= a.d) return;
-  const int i = static_cast<int>(row % a.Sq);
-  const int bh = static_cast<int>(row / a.Sq);
-  const int h = bh % a.H;
-  const int b = bh / a.H;
+  int i, h;
+  const int bh = static_cast<int>(quo_rem(row, a.by_Sq, &i));
+  const int b = static_cast<int>(quo_rem(bh, a.by_H, &h));
   float acc[8];
   if constexpr (DET) {
     const int qb = i / 128;
@@ -290,9 +291,9 @@ __global__ void __launch_bounds__(256) fa_diff_dkv(const DiffBwdArgs a) {
   const int part = static_cast<int>(gid % G);
   const int64_t bhs = static_cast<int64_t>(a.B) * a.Hk;
   if (row >= bhs * a.Sk) return;
-  const int key = static_cast<int>(row % a.Sk);
-  const int bh = static_cast<int>(row / a.Sk);
-  const int hk = bh % a.Hk, b = bh / a.Hk;
+  int key, hk;
+  const int bh = static_cast<int>(quo_rem(row, a.by_Sk, &key));
+  const int b = static_cast<int>(quo_rem(bh, a.by_Hk, &hk));
   const bool is_k = part < 16;
   const int c = part >> 3;  // map, for dK
   const int col = is_k ? (part & 7) * 8 : (part - 16) * 8;
@@ -471,25 +472,29 @@ __global__ void __launch_bounds__(448, 1)
   // Grid order as the plain backward's: with a causal mask key-block-major,
   // the first key blocks (the most query blocks) first; without one
   // head-major.
-  const int hb_count = a.Hk * a.B;
-  const int part = static_cast<int>(blockIdx.x) % a.parts;
-  const int cta = static_cast<int>(blockIdx.x) / a.parts;
-  const int kvb = a.causal ? cta / hb_count : cta % a.nkb;
-  const int hb = a.causal ? cta % hb_count : cta / a.nkb;
-  const int hk = hb % a.Hk;
-  const int b = hb / a.Hk;
-  const int group = a.H / a.Hk;
+  int part, inner, hk;
+  const int cta = static_cast<int>(quo_rem(blockIdx.x, a.by_parts, &part));
+  const int outer = static_cast<int>(quo_rem(cta, a.by_order, &inner));
+  const int kvb = a.causal ? outer : inner;
+  const int b = static_cast<int>(quo_rem(a.causal ? inner : outer, a.by_Hk, &hk));
+  const int group = a.group;
   const int n0 = kvb * 128;
   const int off = a.Sk - a.Sq;
   const int i_start = bwd_first_qblock(kvb, a.Sq, a.Sk, a.causal);
   const int nb = max(0, a.nqb - i_start);  // query blocks of one head
   // This CTA's part of the list of (head, query block) pairs; two chunks each.
   const int64_t listed = static_cast<int64_t>(nb) * group;
-  const int blk0 = static_cast<int>(listed * part / a.parts);
-  const int n = 2 * (static_cast<int>(listed * (part + 1) / a.parts) - blk0);
-  // Chunk i: its head's (b, h) row base and its first query row.
-  auto chunk_bh = [&](int i) { return b * a.H + hk * group + (blk0 + (i >> 1)) / nb; };
-  auto chunk_row = [&](int i) { return (i_start + (blk0 + (i >> 1)) % nb) * 128 + (i & 1) * 64; };
+  int drop;
+  const int blk0 = static_cast<int>(quo_rem(listed * part, a.by_parts, &drop));
+  const int n = 2 * (static_cast<int>(quo_rem(listed * (part + 1), a.by_parts, &drop)) - blk0);
+  // Where chunk 0 lies; the roles walk on from there: its head's (b, h) row base
+  // and its block's first query row.
+  const int head0 = blk0 == 0 ? 0 : blk0 / nb;
+  const int bh0 = b * a.H + hk * group + head0, row0 = (i_start + blk0 - head0 * nb) * 128;
+  auto next_block = [&](int& bh, int& r0) {
+    r0 += 128;
+    if (r0 == a.nqb * 128) r0 = i_start * 128, ++bh;
+  };
   const int64_t acc_rows = static_cast<int64_t>(a.B) * a.H * a.Sq_pad;  // of one map's dQ accumulator
 
   if (threadIdx.x == 0) {
@@ -539,9 +544,10 @@ __global__ void __launch_bounds__(448, 1)
       for (int vb = 0; vb < L::VB; ++vb)
         tma_load_4d(smem + L::OFF_V + vb * L::BLK, &tmV, kv_full, vb * 64, n0, hk, b);
       int nq = 0, nv = 0, no = 0;  // loads issued
+      int bh = bh0, blk_row = row0;
       auto load = [&](int i) -> bool {
         const int qs = i % QS, vs = i % VS;
-        const int bh = chunk_bh(i), r0 = chunk_row(i), h = bh - b * a.H;
+        const int r0 = blk_row + (i & 1) * 64, h = bh - b * a.H;
         // Row terms: free once the softmax warps are through with chunk i - 2.
         if (i >= VS && !wait_bar(ds_ready, (i - VS) & 1, abort_flag, kRoleLoader, i)) return false;
         mbar_arrive_expect_tx(&v_full[vs], kDiffVec * 4);
@@ -561,6 +567,7 @@ __global__ void __launch_bounds__(448, 1)
         for (int vb = 0; vb < L::VB; ++vb)
           tma_load_4d(smem + L::OFF_DO + vb * L::HBLK, &tmdO, o_full, vb * 64, r0, h, b);
         ++no;
+        if (i & 1) next_block(bh, blk_row);
         return true;
       };
       for (int i = 0; i < n && load(i); ++i) {
@@ -736,6 +743,7 @@ __global__ void __launch_bounds__(448, 1)
     constexpr uint32_t kUpper = 16u << 16;  // the warp's lanes 16-31
     const float sl2 = a.scale_log2;
     bool ok = true;
+    int bh = bh0, blk_row = row0;
     for (int i = 0; i < n; ++i) {
       const int vs = i % VS;
       ok = __all_sync(0xffffffffu, wait_bar_c(s_full, i & 1, abort_flag, kRoleSoftmax, i) &&
@@ -744,7 +752,8 @@ __global__ void __launch_bounds__(448, 1)
       tc_fence_after();
       // Query column e of this warpgroup's 32 is masked for key k if e < k + cm0
       // (causal), or if k is past the end.
-      const int cm0 = a.causal ? n0 + wq * 32 - off - chunk_row(i) - 32 * g : -256;
+      const int cm0 = a.causal ? n0 + wq * 32 - off - blk_row - (i & 1) * 64 - 32 * g : -256;
+      if (i & 1) next_block(bh, blk_row);
       const bool masked = cm0 + 31 > 0 || n0 + wq * 32 + 31 >= a.Sk;
       const float* vec = s_vec + vs * kDiffVec + 32 * g + fc;
       // Phase A: p1 = P_1^T, p2 = -lambda P_2^T (fp32, kept), W^T = p1 + p2 in
@@ -918,11 +927,11 @@ __global__ void __launch_bounds__(448, 1)
     const int wq = warp & 3;
     const int tr = wq * 32 + lane;  // TMEM lane = query row of the block
     const uint32_t tDQ = tmem + (static_cast<uint32_t>(wq * 32) << 16) + L::COL_DQ;
+    int bh = bh0, r0 = row0;
     for (int u = 0; u < n; ++u) {  // one use of the dQ buffer per map and block
       if (!__all_sync(0xffffffffu, wait_bar_c(dq_full, u & 1, abort_flag, kRoleSoftmax, u))) break;
       tc_fence_after();
       const int c = u & 1;
-      const int bh = chunk_bh(u), r0 = chunk_row(u & ~1);
       const int swap = (c & (u >> 1)) * 64;  // dQ_2 of an odd block: its halves have changed places
       uint32_t v[2][32];
       tmem_ld32(tDQ, v[0]);
@@ -969,6 +978,7 @@ __global__ void __launch_bounds__(448, 1)
           }
         }
       }
+      if (c == 1) next_block(bh, r0);
     }
     // Let the TMA finish the last reductions before shared memory goes away.
     if (lane == 0) bulk_wait0();
