@@ -82,6 +82,24 @@ int diff_maps(const P* p, int q_rows, CUtensorMap (&m)[5]) {
   return make_map(&m[4], p->v, p->B, p->Sk, p->Hk, p->Dv, p->dtype, 128);
 }
 
+// A programmatic dependent launch: the grid may start while the one before it on
+// the stream still runs, and waits on the device (griddepcontrol.wait) for its end.
+template <typename... K, typename... T>
+int launch_after(void (*kern)(K...), dim3 grid, int threads, int smem, cudaStream_t stream, const T&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 template <int DV, bool BF16>
 int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
   using L = fa::DiffFwdLayout<DV>;
@@ -194,21 +212,9 @@ int launch_diff_rows(const fa_diff_fwd_params* p, const RowsPlan& plan, cudaStre
   kern<<<grid, 256, L::SMEM_ALLOC, stream>>>(mk[0], mk[1], mv, a);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (plan.teams > 0) {
-    // Launched while the pieces are worked on (programmatic dependent launch): its
-    // blocks wait on the device for the whole first grid.
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(unsigned(int64_t(p->B) * p->Hk * a.R));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join, a) != cudaSuccess) return FA_ERR_CUDA;
+    return launch_after(join, dim3(unsigned(int64_t(p->B) * p->Hk * a.R)), 256, 0, stream, a);
   }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return FA_OK;
 }
 
 // Parts that the backward's (head, query block) lists are cut into: the number
@@ -344,19 +350,15 @@ int launch_diff_bwd(const fa_diff_bwd_params* p, cudaStream_t stream) {
   CUtensorMap mdq = m[0];  // not read in deterministic mode
   if (!p->deterministic && (st = make_dq_map(&mdq, a.dq_acc, 2 * rows, 64)) != FA_OK) return st;
   const unsigned grid = unsigned(int64_t(a.nkb) * p->B * p->Hk * a.parts);
-  kern<<<grid, L::kThreads, L::SMEM_ALLOC, stream>>>(m[0], m[1], m[2], m[3], m[4], mdo, mdq, a);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if ((st = launch_after(kern, dim3(grid), L::kThreads, L::SMEM_ALLOC, stream, m[0], m[1], m[2], m[3], m[4], mdo, mdq, a)) != FA_OK) return st;
   if (a.parts > 1) {
     const int64_t threads = int64_t(p->B) * p->Hk * p->Sk * ((128 + DV) / 8);
-    fa::fa_diff_dkv<DV, BF16><<<unsigned((threads + 255) / 256), 256, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if ((st = launch_after(&fa::fa_diff_dkv<DV, BF16>, dim3(unsigned((threads + 255) / 256)), 256, 0, stream, a)) != FA_OK)
+      return st;
   }
   const dim3 dq_grid(unsigned((int64_t(p->B) * p->H * p->Sq * 8 + 255) / 256), 2);
-  if (p->deterministic)
-    fa::fa_diff_dq<BF16, true><<<dq_grid, 256, 0, stream>>>(a);
-  else
-    fa::fa_diff_dq<BF16, false><<<dq_grid, 256, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  st = launch_after(p->deterministic ? &fa::fa_diff_dq<BF16, true> : &fa::fa_diff_dq<BF16, false>, dq_grid, 256, 0, stream, a);
+  if (st != FA_OK) return st;
   return a.dlam != nullptr ? FA_OK : launch_lam(p, a.drow, reinterpret_cast<float*>(ws + w.off_part), stream);
 }
 

@@ -126,6 +126,11 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// The backward's kernels follow each other as programmatic dependent launches:
+// a grid's blocks start as the grid before it runs out of them, and stop here
+// until all of that grid's memory is written and visible. Every block waits, so
+// the end of one grid implies the end of all before it.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -245,6 +250,7 @@ __global__ void __launch_bounds__(256) fa_diff_dq(const DiffBwdArgs a) {
   const int part = static_cast<int>(gid % 8);
   const int c = blockIdx.y;
   const int64_t bhs = static_cast<int64_t>(a.B) * a.H;
+  grid_wait();
   if (row >= bhs * a.Sq || part * 8 >= a.d) return;
   int i, h;
   const int bh = static_cast<int>(quo_rem(row, a.by_Sq, &i));
@@ -290,6 +296,7 @@ __global__ void __launch_bounds__(256) fa_diff_dkv(const DiffBwdArgs a) {
   const int64_t row = gid / G;  // (b, hk, key)
   const int part = static_cast<int>(gid % G);
   const int64_t bhs = static_cast<int64_t>(a.B) * a.Hk;
+  grid_wait();
   if (row >= bhs * a.Sk) return;
   int key, hk;
   const int bh = static_cast<int>(quo_rem(row, a.by_Sk, &key));
@@ -497,7 +504,15 @@ __global__ void __launch_bounds__(448, 1)
   };
   const int64_t acc_rows = static_cast<int64_t>(a.B) * a.H * a.Sq_pad;  // of one map's dQ accumulator
 
-  if (threadIdx.x == 0) {
+  // The loader's thread sets the barriers up itself and asks for the keys at
+  // once: before tensor memory is allocated, and while fa_diff_pre still runs.
+  if (warp == kLoaderWarp && lane == 0) {
+    prefetch_tmap(&tmQ1);
+    prefetch_tmap(&tmQ2);
+    prefetch_tmap(&tmK1);
+    prefetch_tmap(&tmK2);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmdO);
     mbar_init(kv_full, 1);
     for (int s = 0; s < QS; ++s) {
       mbar_init(&q_full[s], 1);
@@ -516,14 +531,14 @@ __global__ void __launch_bounds__(448, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-  }
-  if (warp == kLoaderWarp && lane == 0) {
-    prefetch_tmap(&tmQ1);
-    prefetch_tmap(&tmQ2);
-    prefetch_tmap(&tmK1);
-    prefetch_tmap(&tmK2);
-    prefetch_tmap(&tmV);
-    prefetch_tmap(&tmdO);
+    if (n > 0) {
+      checked(n0 < a.Sk && b < a.B && hk < a.Hk, 510);
+      mbar_arrive_expect_tx(kv_full, (2 + L::VB) * L::BLK);
+      tma_load_4d(smem + L::OFF_K, &tmK1, kv_full, 0, n0, hk, b);
+      tma_load_4d(smem + L::OFF_K + L::BLK, &tmK2, kv_full, 0, n0, hk, b);
+      for (int vb = 0; vb < L::VB; ++vb)
+        tma_load_4d(smem + L::OFF_V + vb * L::BLK, &tmV, kv_full, vb * 64, n0, hk, b);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, L::TMEM_COLS);
@@ -533,16 +548,11 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();  // fa_diff_pre's row terms and cleared accumulators are there
 
   if (warp == kLoaderWarp) {
     // ------------------------------------------------------------------ loader
     if (lane == 0 && n > 0) {
-      checked(n0 < a.Sk && b < a.B && hk < a.Hk, 510);
-      mbar_arrive_expect_tx(kv_full, (2 + L::VB) * L::BLK);
-      tma_load_4d(smem + L::OFF_K, &tmK1, kv_full, 0, n0, hk, b);
-      tma_load_4d(smem + L::OFF_K + L::BLK, &tmK2, kv_full, 0, n0, hk, b);
-      for (int vb = 0; vb < L::VB; ++vb)
-        tma_load_4d(smem + L::OFF_V + vb * L::BLK, &tmV, kv_full, vb * 64, n0, hk, b);
       int nq = 0, nv = 0, no = 0;  // loads issued
       int bh = bh0, blk_row = row0;
       auto load = [&](int i) -> bool {
