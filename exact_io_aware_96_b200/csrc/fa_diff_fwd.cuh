@@ -130,8 +130,8 @@ struct DiffFwdLayout {
   static constexpr int OFF_LSUM = OFF_PMAX + 2 * 2 * 2 * 128 * 4;  // [map][half][row]
   static constexpr int OFF_M = OFF_LSUM + 2 * 2 * 128 * 4;    // [map][row]
   static constexpr int OFF_BAR = OFF_M + 2 * 128 * 4;
-  // q_full, k_full/k_empty[KS], v_full/v_empty[VS], s_full[2], p_full[2], o_final[2], drain
-  static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 6 + 1;
+  // q_full, k_full/k_empty[KS], v_full/v_empty[VS], s_full[2][2], p_full[2], o_final[2], drain
+  static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM_ALLOC = BYTES + 1024;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(576, 1)
   uint64_t* v_full = k_empty + KS;
   uint64_t* v_empty = v_full + VS;
   uint64_t* s_full = v_empty + VS;
-  uint64_t* p_full = s_full + 2;
+  uint64_t* p_full = s_full + 4;
   uint64_t* o_final = p_full + 2;
   uint64_t* drain = o_final + 2;
   float* pmax = reinterpret_cast<float*>(smem + L::OFF_PMAX);
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(576, 1)
       mbar_init(&v_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
+      mbar_init(&s_full[2 * t], 1);
+      mbar_init(&s_full[2 * t + 1], 1);
       mbar_init(&p_full[t], 8);  // one arrival per softmax warp of the map
       mbar_init(&o_final[t], 1);
     }
@@ -259,21 +260,22 @@ __global__ void __launch_bounds__(576, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity, int iter) {
         return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, kRoleMma, iter));
       };
-      constexpr uint32_t idS = idesc_f16(BF16, 128, 128, 0, 0);
+      constexpr uint32_t idS = idesc_f16(BF16, 128, 64, 0, 0);
       constexpr uint32_t idO = idesc_f16(BF16, 128, DV, 0, 1);
       const uint32_t sQ = smem_u32(smem + L::OFF_Q);
       const uint32_t sK = smem_u32(smem + L::OFF_K);
       const uint32_t sV = smem_u32(smem + L::OFF_V);
-      auto issue_S = [&](int t, int ks) {
+      auto issue_S = [&](int t, int hf, int ks) {
         const uint64_t qd = desc_sw128(sQ + t * L::BLK, 16, 1024);
-        const uint64_t kd = desc_sw128(sK + (ks * 2 + t) * L::BLK, 16, 1024);
+        const uint64_t kd = desc_sw128(sK + (ks * 2 + t) * L::BLK + hf * (L::BLK / 2), 16, 1024);
         uint64_t ad[4], bd[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           ad[u] = desc_add(qd, u * 32);
           bd[u] = desc_add(kd, u * 32);
         }
-        mma_ss_x4(tmem + 128 * t, ad, bd, idS, 0);
+        mma_ss_x4(tmem + 128 * t + 64 * hf, ad, bd, idS, 0);
+        mma_commit_w(&s_full[2 * t + hf]);
       };
       auto issue_PV = [&](int t, int vs, int acc) {
         const uint64_t vd = desc_sw128(sV + vs * L::VB * L::BLK, L::BLK, 1024);
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(576, 1)
           uint64_t vb[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            pa[u] = tmem + 128 * t + 64 * hf + u * 8;
+            pa[u] = tmem + 128 * t + 64 + 32 * hf + u * 8;
             vb[u] = desc_add(vd, (4 * hf + u) * 2048);
           }
           mma_ts_x4(tmem + L::OBASE + t * DV, pa, vb, idO, (acc || hf > 0) ? 1u : 0u);
@@ -293,8 +295,8 @@ __global__ void __launch_bounds__(576, 1)
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < 2; ++t) {
-          issue_S(t, 0);
-          mma_commit_w(&s_full[t]);
+          issue_S(t, 0, 0);
+          issue_S(t, 1, 0);
         }
         mma_commit_w(&k_empty[0]);
       }
@@ -307,12 +309,12 @@ __global__ void __launch_bounds__(576, 1)
         for (int t = 0; t < 2; ++t) {
           if (!ok || !(ok = wait(&p_full[t], j & 1, j))) break;
           tc_fence_after();
+          if (jn < n) issue_S(t, 0, ksn);
           issue_PV(t, vs, j > 0);
           if (j == n - 1) mma_commit_w(&o_final[t]);
           if (t == 1) mma_commit_w(&v_empty[vs]);
           if (jn < n) {
-            issue_S(t, ksn);
-            mma_commit_w(&s_full[t]);
+            issue_S(t, 1, ksn);
             if (t == 1) mma_commit_w(&k_empty[ksn]);
           }
         }
@@ -331,6 +333,7 @@ __global__ void __launch_bounds__(576, 1)
     const int pair_bar = 1 + t * 4 + quarter;  // named barrier of the two warps that share these rows
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128 * t + 64 * c;
+    const uint32_t tP = tmem + lane_base + 128 * t + 64 + 32 * c;
     const uint32_t tO = tmem + lane_base + L::OBASE + t * DV + c * (DV / 2);  // the half this warp rescales
     const float sl2 = a.scale_log2;
     const int off = sk - a.Sq;
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(576, 1)
     for (int j = 0; j < n; ++j) {
       // `ok` false here: a wait of the previous block ran out; this warp goes
       // straight to the pair barrier, which then ends both warps.
-      const bool ready = ok && __all_sync(0xffffffffu, wait_bar(&s_full[t], j & 1, abort_flag, kRoleSoftmax, j));
+      const bool ready = ok && __all_sync(0xffffffffu, wait_bar(&s_full[2 * t + c], j & 1, abort_flag, kRoleSoftmax, j));
       const int k0 = j * 128 + 64 * c;  // first key of this half
       const bool masked = k0 + 64 > sk || (a.causal && k0 + 63 > q0 + off);
       int lim = sk - 1 - k0;  // last allowed column of this half
@@ -398,8 +401,11 @@ __global__ void __launch_bounds__(576, 1)
       // ahead with the old one, and the two warps meet afterwards, when neither
       // has to wait long; if a row of either half asks for a raise, O_t is
       // rescaled and the pass is made again.
+      tc_fence_before();
       if (!named_bar_and(pair_bar, 64, keep)) {
-        if (!named_bar_and(pair_bar, 64, ready)) {
+        const bool in = ready && __all_sync(0xffffffffu, wait_bar(&s_full[2 * t + 1], j & 1, abort_flag, kRoleSoftmax, j));
+        tc_fence_after();
+        if (!named_bar_and(pair_bar, 64, in)) {
           ok = false;
           break;
         }
@@ -425,10 +431,13 @@ __global__ void __launch_bounds__(576, 1)
           }
         }
         pass(std::true_type{});
+        tc_fence_before();
+        named_bar_and(pair_bar, 64, true);
       }
+      tc_fence_after();
       l += add;
-      tmem_st16(tS, pw[0]);  // over this half's own columns of S
-      tmem_st16(tS + 16, pw[1]);
+      tmem_st16(tP, pw[0]);  // over the second half's S, which the pair has read
+      tmem_st16(tP + 16, pw[1]);
       if (t == 0 && a.k_lens != nullptr && j == n - 1 && (j + 1) * 128 > sk) {
         // V rows past this sequence's last key (whatever a cache holds there)
         // become zeros before P V reads them: their P is 0, but 0 x inf is
