@@ -130,8 +130,8 @@ struct DiffFwdLayout {
   static constexpr int OFF_LSUM = OFF_PMAX + 2 * 2 * 2 * 128 * 4;  // [map][half][row]
   static constexpr int OFF_M = OFF_LSUM + 2 * 2 * 128 * 4;    // [map][row]
   static constexpr int OFF_BAR = OFF_M + 2 * 128 * 4;
-  // q_full, k_full/k_empty[KS], v_full/v_empty[VS], s_full[2][2], p_full[2], o_final[2], drain
-  static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 8 + 1;
+  // q_full, k_full/k_empty[KS], v_full/v_empty[VS], s_full[2][2], s_free[2], p_full[2], o_final[2], drain
+  static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 10 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM_ALLOC = BYTES + 1024;
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(576, 1)
   uint64_t* v_full = k_empty + KS;
   uint64_t* v_empty = v_full + VS;
   uint64_t* s_full = v_empty + VS;
-  uint64_t* p_full = s_full + 4;
+  uint64_t* s_free = s_full + 4;
+  uint64_t* p_full = s_free + 2;
   uint64_t* o_final = p_full + 2;
   uint64_t* drain = o_final + 2;
   float* pmax = reinterpret_cast<float*>(smem + L::OFF_PMAX);
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(576, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[2 * t], 1);
       mbar_init(&s_full[2 * t + 1], 1);
+      mbar_init(&s_free[t], 4);  // one arrival per warp of the first half
       mbar_init(&p_full[t], 8);  // one arrival per softmax warp of the map
       mbar_init(&o_final[t], 1);
     }
@@ -307,9 +309,14 @@ __global__ void __launch_bounds__(576, 1)
         if (jn < n && !(ok = wait(&k_full[ksn], (jn / KS) & 1, jn))) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!ok || !(ok = wait(&p_full[t], j & 1, j))) break;
+          if (!ok) break;
+          if (jn < n) {
+            if (!(ok = wait(&s_free[t], j & 1, j))) break;
+            tc_fence_after();
+            issue_S(t, 0, ksn);
+          }
+          if (!(ok = wait(&p_full[t], j & 1, j))) break;
           tc_fence_after();
-          if (jn < n) issue_S(t, 0, ksn);
           issue_PV(t, vs, j > 0);
           if (j == n - 1) mma_commit_w(&o_final[t]);
           if (t == 1) mma_commit_w(&v_empty[vs]);
@@ -435,6 +442,7 @@ __global__ void __launch_bounds__(576, 1)
         named_bar_and(pair_bar, 64, true);
       }
       tc_fence_after();
+      if (c == 0 && lane == 0 && j + 1 < n) mbar_arrive(&s_free[t]);
       l += add;
       tmem_st16(tP, pw[0]);  // over the second half's S, which the pair has read
       tmem_st16(tP + 16, pw[1]);
