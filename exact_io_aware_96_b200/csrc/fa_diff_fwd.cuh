@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(576, 1)
       bool keep = ready;
       // P, its sum and the row's maximum in one pass over this half's S, 32
       // columns at a time, with the maximum of the blocks before.
-      auto pass = [&](auto masked_t) {
+      auto pass = [&](auto masked_t, auto max_only_t) {
         constexpr bool M = decltype(masked_t)::value;
         const float mu = (m == -INFINITY) ? 0.f : m;
         const uint64_t negmu2 = f2(-mu, -mu);
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(576, 1)
             mx2 = max3(mx2, xf(i + 4), xf(i + 5));
             mx3 = max3(mx3, xf(i + 6), xf(i + 7));
           }
-          fwd_exp32<BF16, M>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
+          if constexpr (!decltype(max_only_t)::value) fwd_exp32<BF16, M>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
         }
         pm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
         float a0, a1;
@@ -395,14 +395,16 @@ __global__ void __launch_bounds__(576, 1)
       };
       if (ready) {
         tc_fence_after();
-        if (masked)
-          pass(std::true_type{});
+        if (j == 0)
+          pass(std::true_type{}, std::true_type{});  // there is no maximum to go ahead with
+        else if (masked)
+          pass(std::true_type{}, std::false_type{});
         else
-          pass(std::false_type{});
+          pass(std::false_type{}, std::false_type{});
         // Written again in block j + 2, after the partner has passed the
         // barrier of block j + 1, i.e. after it has read this value.
         slot[c * 128 + r] = pm;
-        keep = !(pm * sl2 > m + 8.0f);
+        keep = j > 0 && !(pm * sl2 > m + 8.0f);
       }
       // The maximum is raised in few blocks. So the exponentials above have gone
       // ahead with the old one, and the two warps meet afterwards, when neither
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(576, 1)
             tmem_st32(tO + 32 * q, ov);
           }
         }
-        pass(std::true_type{});
+        pass(std::true_type{}, std::false_type{});
         tc_fence_before();
         named_bar_and(pair_bar, 64, true);
       }
