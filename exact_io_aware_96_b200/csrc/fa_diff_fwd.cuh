@@ -28,17 +28,24 @@
 //              32r .. 32r + 31, one query row per thread
 //   warp  16   TMA loader: Q_1, Q_2 once, then (K_1, K_2)_j and V_j into rings
 //   warp  17   MMA issuer
-// Tensor memory: [128t, 128t + 128) S_t, then P_t   [256 + t DV, + DV) O_t
+// Tensor memory: [128t, 128t + 64) S_t of keys 0 .. 63, [128t + 64, 128t + 128)
+//   S_t of keys 64 .. 127, then P_t of the whole block  [256 + t DV, + DV) O_t
+// P_t lies over the second half's scores alone. The first half's are free once
+// their warps have read them, so S_t(j + 1) of that half is made before P V(j),
+// and its softmax runs under P V(j) and the second half's S_t(j + 1).
 //
-// What bounds it: per 128 x 128 block the products take 4 x 128 x 128 x (64 +
-// DV) flops (1550 tensor cycles at DV = 128) and the softmax 2 x 128 x 128
+// What bounds it: per 128 x 128 block the products take 1820 tensor cycles (S in
+// four N = 64 products of 195, P V in two of 520) and the softmax 2 x 128 x 128
 // exponentials (2048 MUFU cycles, 1536 with a quarter of them moved to the FMA
-// pipe); a map's chain of softmax, P V and the next S overlaps the other map's
-// only. Measured at B = 1, H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 244
-// us, 845 TFLOP/s (252 us with the warps meeting before the exponentials); with
-// the softmax left out the same grid takes 160 us, with free exponentials 213.
-// 64-key blocks in two buffers per map, so that a map's next S is ready early,
-// took 356 us: twice as many hand-offs.
+// pipe) and 1600 issue slots per scheduler; a block takes about 2900. A map's
+// chain of P V, the second half's S and softmax, and the hand-offs between them
+// (a wake-up is about 300 cycles) overlaps the other map's and the first half's
+// only. Measured at B = 1, H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 208
+// us, 991 TFLOP/s; 225 with S in one N = 128 product after P V, 214 with the
+// first half's next S made when all of P is there, 212 with the first block's
+// exponentials computed twice. Slower: 64-key blocks in two buffers per map (356
+// us), an issuing warp per map (299), the first half's warps taking 80 keys of
+// the 128 (213 against 212), waits out of line (222 against 208).
 #pragma once
 
 #include <type_traits>
@@ -425,8 +432,8 @@ __global__ void __launch_bounds__(576, 1)
           m = m_blk;
         }
         l *= alpha;
-        // S_t(j) was issued after P_t(j-1) V_{j-1}, so s_full covers both and
-        // O_t may be rescaled now.
+        // The second half's S_t(j) was issued after P_t(j-1) V_{j-1}, so its
+        // barrier covers both and O_t may be rescaled now.
         if (j > 0) {
 #pragma unroll 1
           for (int q = 0; q < DV / 64; ++q) {
