@@ -121,7 +121,7 @@ int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
   a.lam_kind = lam_kind(p->lambda);
   a.k_lens = p->k_lens;
   a.B = p->B, a.H = p->H, a.Hk = p->Hk, a.Sq = p->Sq, a.Sk = p->Sk;
-  a.dv = p->Dv;
+  a.d = p->D, a.dv = p->Dv;
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.causal = p->causal;
   a.n_qblocks = (p->Sq + 127) / 128;

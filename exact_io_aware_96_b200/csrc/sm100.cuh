@@ -312,6 +312,24 @@ __device__ __forceinline__ void mma_ss_x4(uint32_t d_tmem, const uint64_t (&a)[4
       "r"(accum)
       : "memory");
 }
+// The first n (1 .. 4) of them.
+__device__ __forceinline__ void mma_ss_up_to_4(uint32_t d_tmem, const uint64_t (&a)[4], const uint64_t (&b)[4],
+                                               uint32_t idesc, uint32_t accum, int n) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, q;\n\t"
+      "setp.ne.b32 p, %10, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n\t"
+      "setp.gt.and.s32 q, %11, 1, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, 1;\n\t"
+      "setp.gt.and.s32 q, %11, 2, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, 1;\n\t"
+      "setp.gt.and.s32 q, %11, 3, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, 1;\n\t}\n" ::"r"(d_tmem),
+      "l"(a[0]), "l"(a[1]), "l"(a[2]), "l"(a[3]), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "r"(idesc),
+      "r"(accum), "r"(n)
+      : "memory");
+}
 __device__ __forceinline__ void mma_ts_x4(uint32_t d_tmem, const uint32_t (&a)[4], const uint64_t (&b)[4],
                                           uint32_t idesc, uint32_t accum) {
   asm volatile(
