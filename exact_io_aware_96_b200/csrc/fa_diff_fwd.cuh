@@ -368,69 +368,78 @@ __global__ void __launch_bounds__(576, 1)
       if (a.causal) lim = min(lim, row + off - k0);
       float* slot = pmax + (((j & 1) * 2 + t) * 2) * 128;
       const uint64_t sl2x2 = f2(sl2, sl2);
-      float pm = -INFINITY, add = 0.f;
+      float add = 0.f;
       uint32_t pw[2][16];  // P, two keys to a word
-      bool keep = ready;
-      // P, its sum and the row's maximum in one pass over this half's S, 32
-      // columns at a time, with the maximum of the blocks before.
-      auto pass = [&](auto masked_t, auto max_only_t) {
+      // P and its sum in one pass over this half's S, 32 columns at a time, with
+      // the maximum of the blocks before; returns whether that maximum will do.
+      auto pass = [&](auto masked_t) -> bool {
         constexpr bool M = decltype(masked_t)::value;
         const float mu = (m == -INFINITY) ? 0.f : m;
         const uint64_t negmu2 = f2(-mu, -mu);
         uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+        float mx = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t sv[32];
           tmem_ld32(tS + 32 * q, sv);
           tmem_ld_wait();
           reg_fence(sv);
-          auto xf = [&](int i) {
-            const float x = __uint_as_float(sv[i]);
-            return !M || 32 * q + i <= lim ? x : -INFINITY;
-          };
+          if constexpr (!M) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            mx0 = max3(mx0, xf(i), xf(i + 1));
-            mx1 = max3(mx1, xf(i + 2), xf(i + 3));
-            mx2 = max3(mx2, xf(i + 4), xf(i + 5));
-            mx3 = max3(mx3, xf(i + 6), xf(i + 7));
+            for (int i = 0; i < 16; ++i)
+              if (fwd_pair_on_fma(i)) mx = max3(mx, __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
           }
-          if constexpr (!decltype(max_only_t)::value) fwd_exp32<BF16, M>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
+          fwd_exp32<BF16, M>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
         }
-        pm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
         float a0, a1;
         f2_split(add2(acc0, acc1), a0, a1);
         add = a0 + a1;
+        return m != -INFINITY && !(add > 256.f) && !(mx * sl2 > m + 8.f);
       };
-      if (ready) {
+      bool keep = false;  // the first block has no maximum to go ahead with
+      if (ready && j > 0) {
         tc_fence_after();
-        if (j == 0)
-          pass(std::true_type{}, std::true_type{});  // there is no maximum to go ahead with
-        else if (masked)
-          pass(std::true_type{}, std::false_type{});
-        else
-          pass(std::false_type{}, std::false_type{});
-        // Written again in block j + 2, after the partner has passed the
-        // barrier of block j + 1, i.e. after it has read this value.
-        slot[c * 128 + r] = pm;
-        keep = j > 0 && !(pm * sl2 > m + 8.0f);
+        keep = masked ? pass(std::true_type{}) : pass(std::false_type{});
       }
       // The maximum is raised in few blocks. So the exponentials above have gone
       // ahead with the old one, and the two warps meet afterwards, when neither
-      // has to wait long; if a row of either half asks for a raise, O_t is
+      // has to wait long. While a half's sum is at most 256, each of its P is: no
+      // row maximum is needed to know that the old one will do. (A pair on the
+      // FMA pipe may be anything past 2^128; its scores are looked at.) If a row
+      // of either half asks for a raise, the block's maximum is taken, O_t is
       // rescaled and the pass is made again.
       tc_fence_before();
       if (!named_bar_and(pair_bar, 64, keep)) {
         const bool in = ready && __all_sync(0xffffffffu, wait_bar(&s_full[2 * t + 1], j & 1, abort_flag, kRoleSoftmax, j));
         tc_fence_after();
+        float pm = -INFINITY;
+        if (in) {
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            uint32_t sv[32];
+            tmem_ld32(tS + 32 * q, sv);
+            tmem_ld_wait();
+            reg_fence(sv);
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+            auto xf = [&](int i) { return 32 * q + i <= lim ? __uint_as_float(sv[i]) : -INFINITY; };
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              mx0 = max3(mx0, xf(i), xf(i + 1));
+              mx1 = max3(mx1, xf(i + 2), xf(i + 3));
+            }
+            pm = max3(pm, mx0, mx1);
+          }
+          // Written again in block j + 2 at the earliest, after the partner has
+          // passed a barrier of block j + 1, i.e. after it has read this value.
+          slot[c * 128 + r] = pm;
+        }
         if (!named_bar_and(pair_bar, 64, in)) {
           ok = false;
           break;
         }
         const float m_blk = fmaxf(pm, slot[(c ^ 1) * 128 + r]) * sl2;
         float alpha = 1.f;
-        if (m_blk > m + 8.0f) {
+        if (m_blk > m) {
           alpha = ex2(m - m_blk);  // 0 when m was -inf
           m = m_blk;
         }
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(576, 1)
             tmem_st32(tO + 32 * q, ov);
           }
         }
-        pass(std::true_type{}, std::false_type{});
+        pass(std::true_type{});
         tc_fence_before();
         named_bar_and(pair_bar, 64, true);
       }

@@ -107,6 +107,8 @@ struct FwdLayout {
 // packed to 16 words of two 16-bit values; adds the P values into acc0/acc1.
 // MASKED: entries past column `lim` are -inf (P = 0) and every exponential
 // runs on the MUFU unit, which returns exactly 0 for them.
+// Which of the pairs go to the FMA pipe where nothing is masked.
+__device__ constexpr bool fwd_pair_on_fma(int cc) { return (cc & 3) == 3; }
 template <bool BF16, bool MASKED>
 __device__ __forceinline__ void fwd_exp32(const uint32_t (&sv)[32], int col0, int lim, uint64_t sl2x2,
                                           uint64_t negmu2, uint64_t& acc0, uint64_t& acc1, uint32_t (&pw)[16]) {
@@ -121,7 +123,7 @@ __device__ __forceinline__ void fwd_exp32(const uint32_t (&sv)[32], int col0, in
     }
     const uint64_t tt = fma2(f2(s0, s1), sl2x2, negmu2);
     uint64_t e;
-    if (!MASKED && (cc & 3) == 3) {
+    if (!MASKED && fwd_pair_on_fma(cc)) {
       e = exp2_poly2(tt);
     } else {
       float t0, t1;
