@@ -131,6 +131,34 @@ def test_wide_scores(fa_lib):
     full_check(case(1, 640, 640, 2, 2, 64, 128, torch.float16, 10, std=3.0), True)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("jump", [4.5, 5.5, 7.0, 90.0, 200.0, 2000.0])
+@pytest.mark.parametrize("whole", [False, True])
+def test_a_late_key_raises_the_maximum(fa_lib, jump, whole, dtype):
+    """One key of the third block (every column of it, one to a head), or all of
+    them, scores `jump` above the rest: past the point where the old maximum will
+    do, past 2^128 where an exponential on the FMA pipe is anything, or just
+    below. q is a unit vector, so scores are k's first column, without rounding."""
+    B, H, Sq, Sk, D, Dv = 4, 32, 32, 512, 8, 16
+    q, k, v, lam, _ = case(B, Sq, Sk, H, H, D, Dv, dtype, 31)
+    q.zero_()
+    q[..., 0] = 1
+    k.clamp_(-1, 1)
+    for b in range(B):
+        for h in range(H):
+            col = b * H + h
+            for c in range(2):
+                at = slice(256, 384) if whole else 256 + (col if c == 0 else 127 - col)
+                k[b, at, h, c, 0] = jump
+    u, t = ROUND[dtype]
+    want = differential(np64(q), np64(k), np64(v), np64(lam), 1.0, False, None, u=u, t=t)
+    o, lse, o2 = fa.diff_forward(*(x.cuda() for x in (q, k, v, lam)), scale=1.0, need_o2=True)
+    status_clear()
+    check_lse(lse, want["lse"])
+    within("o", o, want["o"], want["o_bound"])
+    within("o2", o2, want["o2"], want["o2_bound"])
+
+
 def test_strided_views_and_given_outputs(fa_lib):
     """q, k, v as slices of one projection, gradients into slices of another."""
     B, S, H, D, Dv = 2, 140, 2, 64, 128
