@@ -326,17 +326,19 @@ __global__ void __launch_bounds__(256) fa_diff_dkv(const DiffBwdArgs a) {
 }
 
 // ----------------------------------------------------------- dlambda sums
-// dlambda has extents ext[] (each 1 or the full axis; order batch, row, head)
+// dlambda has lambda's extents (each 1 or the full axis; order batch, row, head)
 // and is dense. Element x sums drow over the axes with extent 1: `count` terms,
 // cut into `parts` runs. One block per (element, run) writes its sum to
 // part[element * parts + run], in a fixed order.
+constexpr int kLamThreads = 512;
 struct LamSumArgs {
   const float* drow;  // [B][H][Sq]
   float* part;
   void* dlam;
   int dlam_kind;
   int B, H, Sq;
-  int ext[3];
+  Div by_s, by_h;    // lambda's extents along rows and heads
+  Div by_ns, by_nh;  // rows and heads that one of its elements sums over
   int64_t n_out, count;
   int parts;
 };
@@ -353,35 +355,52 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
   return r;
 }
 
-// Term k of element x's sum. The summed axes, innermost first: rows, heads, batch.
-__device__ __forceinline__ float lam_term(const LamSumArgs& a, int64_t x, int64_t k) {
-  const int eh = static_cast<int>(x % a.ext[2]);
-  const int64_t y = x / a.ext[2];
-  const int es = static_cast<int>(y % a.ext[1]), eb = static_cast<int>(y / a.ext[1]);
-  const int ns = a.ext[1] == 1 ? a.Sq : 1, nh = a.ext[2] == 1 ? a.H : 1;
-  const int64_t s = k % ns, z = k / ns;
-  const int64_t h = z % nh, b = z / nh;
-  return a.drow[((eb + b) * a.H + eh + h) * a.Sq + es + s];
+// Element x's place, and term k of its sum. The summed axes, innermost first:
+// rows, heads, batch.
+__device__ __forceinline__ const float* lam_base(const LamSumArgs& a, int64_t x) {
+  int eh, es;
+  const int64_t eb = quo_rem(quo_rem(x, a.by_h, &eh), a.by_s, &es);
+  return a.drow + (eb * a.H + eh) * a.Sq + es;
+}
+__device__ __forceinline__ float lam_term(const LamSumArgs& a, const float* base, int64_t k) {
+  int s, h;
+  const int64_t b = quo_rem(quo_rem(k, a.by_ns, &s), a.by_nh, &h);
+  return base[(b * a.H + h) * a.Sq + s];
+}
+__device__ __forceinline__ float lam_term(const LamSumArgs& a, const float* base, int k) {
+  const int z = quo(k, a.by_ns), b = quo(z, a.by_nh);
+  const int s = k - z * a.by_ns.d, h = z - b * a.by_nh.d;
+  return base[(static_cast<int64_t>(b) * a.H + h) * a.Sq + s];
+}
+// Terms lo + first, lo + first + step, ... below hi, in this order.
+__device__ __forceinline__ float lam_terms(const LamSumArgs& a, const float* base, int64_t lo, int64_t hi, int first,
+                                           int step) {
+  float v = 0.f;
+  if (hi < (int64_t(1) << 31) - step) {
+#pragma unroll 8
+    for (int k = static_cast<int>(lo) + first; k < static_cast<int>(hi); k += step) v += lam_term(a, base, k);
+  } else {
+    for (int64_t k = lo + first; k < hi; k += step) v += lam_term(a, base, k);
+  }
+  return v;
 }
 
 // Few terms: one thread per element.
 __global__ void __launch_bounds__(256) fa_diff_lam_few(const LamSumArgs a) {
   const int64_t x = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (x >= a.n_out) return;
-  float v = 0.f;
-  for (int64_t k = 0; k < a.count; ++k) v += lam_term(a, x, k);
-  store_lam(a.dlam, a.dlam_kind, x, v);
+  grid_wait();
+  if (x < a.n_out) store_lam(a.dlam, a.dlam_kind, x, lam_terms(a, lam_base(a, x), 0, a.count, 0, 1));
 }
 
-__global__ void __launch_bounds__(256) fa_diff_lam_part(const LamSumArgs a) {
-  __shared__ float sm[8];
+__global__ void __launch_bounds__(kLamThreads) fa_diff_lam_part(const LamSumArgs a) {
+  __shared__ float sm[kLamThreads / 32];
   const int64_t x = blockIdx.x / a.parts;
   const int run = static_cast<int>(blockIdx.x % a.parts);
   const int64_t len = (a.count + a.parts - 1) / a.parts;
   const int64_t lo = run * len, hi = min(a.count, lo + len);
-  float v = 0.f;
-  for (int64_t k = lo + threadIdx.x; k < hi; k += 256) v += lam_term(a, x, k);
-  v = block_sum<256>(v, sm);
+  const float* base = lam_base(a, x);
+  grid_wait();
+  const float v = block_sum<kLamThreads>(lam_terms(a, base, lo, hi, threadIdx.x, kLamThreads), sm);
   if (threadIdx.x == 0) {
     if (a.parts == 1)
       store_lam(a.dlam, a.dlam_kind, x, v);
@@ -393,6 +412,7 @@ __global__ void __launch_bounds__(256) fa_diff_lam_part(const LamSumArgs a) {
 __global__ void __launch_bounds__(256) fa_diff_lam_sum(const LamSumArgs a) {
   __shared__ float sm[8];
   float v = 0.f;
+  grid_wait();
   for (int k = threadIdx.x; k < a.parts; k += 256) v += a.part[static_cast<int64_t>(blockIdx.x) * a.parts + k];
   v = block_sum<256>(v, sm);
   if (threadIdx.x == 0) store_lam(a.dlam, a.dlam_kind, blockIdx.x, v);

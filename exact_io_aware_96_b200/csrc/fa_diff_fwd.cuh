@@ -18,10 +18,11 @@
 //
 // The online softmax and the exponentials (one pair in four on the FMA pipe
 // where no entry is masked) are those of fa_fwd.cuh. The running maximum is
-// raised only when a block's exceeds it by more than 8, which happens in few
-// blocks; the exponentials therefore go ahead with the maximum of the blocks
+// raised in few blocks: the exponentials go ahead with the maximum of the blocks
 // before, in one pass over S, and the two warps that share a row meet after
-// them. A block that does ask for a raise is passed over again.
+// them. The block's own maximum is not even taken: a half's sum of at most 256
+// says that no P is above 2^8. A block that does ask for a raise (the first one
+// always does) has its maximum taken and is passed over again.
 //
 // Warp roles (576 threads):
 //   warps 8t + 4c + r  softmax of map t, key half c of every block, TMEM lanes
@@ -37,15 +38,18 @@
 // What bounds it: per 128 x 128 block the products take 1820 tensor cycles (S in
 // four N = 64 products of 195, P V in two of 520) and the softmax 2 x 128 x 128
 // exponentials (2048 MUFU cycles, 1536 with a quarter of them moved to the FMA
-// pipe) and 1600 issue slots per scheduler; a block takes about 2900. A map's
+// pipe) and 1500 issue slots per scheduler; a block takes about 2700. A map's
 // chain of P V, the second half's S and softmax, and the hand-offs between them
 // (a wake-up is about 300 cycles) overlaps the other map's and the first half's
-// only. Measured at B = 1, H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 208
-// us, 991 TFLOP/s; 225 with S in one N = 128 product after P V, 214 with the
-// first half's next S made when all of P is there, 212 with the first block's
-// exponentials computed twice. Slower: 64-key blocks in two buffers per map (356
-// us), an issuing warp per map (299), the first half's warps taking 80 keys of
-// the 128 (213 against 212), waits out of line (222 against 208).
+// only. Measured at B = 1, H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 198
+// us, 1041 TFLOP/s; 208 with the maximum of every block taken, 212 with the first
+// block's exponentials computed twice, 214 with the first half's next S made when
+// all of P is there, 225 with S in one N = 128 product after P V. Slower: 64-key
+// blocks in two buffers per map (356 us), an issuing warp per map (299), the first
+// half's warps taking 80 keys of the 128 (213 against 212), waits out of line (222
+// against 208), P in columns of its own where DV = 64 leaves room (60 against 56),
+// no exponentials on the FMA pipe, or three pairs in eight (210 and 215 against
+// 208).
 #pragma once
 
 #include <type_traits>
