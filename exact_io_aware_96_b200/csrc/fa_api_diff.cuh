@@ -137,14 +137,17 @@ int launch_diff_fwd(const fa_diff_fwd_params* p, cudaStream_t stream) {
 // small, as many teams as fit at once share the keys evenly; large teams get a
 // few waves, which even out by themselves. "Direct" saves the second kernel and
 // the restart between batch entries (about 8 and 4 us), but leaves an entry's
-// keys to one CTA, which takes 18 ns a key alone and 28 on a full GPU; it is
-// taken where that is estimated 15% shorter, and for caches of two units per
-// stream at most. Measured, us, direct against teams (D = 64, DV = 128): 32
-// entries x 8 heads x 500 keys 16.7 / 21.7; 8 x 8 x 1000 22.5 / 15.8; 1 x 8 x
-// 1000 22.0 / 8.2.
+// keys to one CTA, which takes 18 ns a key alone and 28 on a full GPU, or to a
+// cluster of 2, 4 or 8, which join their pieces out of each other's shared memory
+// (1 us more). It is taken where that is estimated 15% shorter, and for caches of
+// two units per stream at most. Measured, us (D = 64, DV = 128), one CTA /
+// cluster / teams: 32 entries x 8 heads x 500 keys 16.7 / - / 21.7; 8 x 8 x 1000
+// 22.5 / 12.5 / 15.8; 1 x 8 x 1000 22.0 / 8.0 / 8.1 (in one launch instead of
+// two); 16 x 2 x 300 10.5 / 7.9 / -; 1 x 8 x 2000 - / - / 9.1.
 struct RowsPlan {
   bool rows = false;  // false: the tiled kernel
   int teams = 0;      // 0: direct
+  int cluster = 1;    // direct: CTAs that share an entry's keys
   uint64_t off_o = 0, bytes = 0;
 };
 RowsPlan rows_plan(int B, int H, int Hk, int Sq, int Sk, int Dv) {
@@ -156,11 +159,17 @@ RowsPlan rows_plan(int B, int H, int Hk, int Sq, int Sk, int Dv) {
   p.rows = true;
   const int64_t items = team * B;
   const int64_t teams = team * 4 <= slots ? slots / team : (4 * slots + team - 1) / team;
-  const double full = std::min(1.0, double(items) / double(slots)), waves = double((items + slots - 1) / slots);
-  const double direct_us = waves * (4 + Sk * std::max(0.018, 0.028 * full));
+  double direct_us = 0;
+  for (int T = 1; T <= 8 && (T == 1 || T * 64 <= Sk); T *= 2) {
+    const int64_t ctas = items * T;
+    const double full = std::min(1.0, double(ctas) / double(slots)), waves = double((ctas + slots - 1) / slots);
+    const double us = waves * ((T == 1 ? 4 : 5) + double(Sk) / T * std::max(0.018, 0.028 * full));
+    if (T == 1 || us < 0.95 * direct_us) direct_us = us, p.cluster = T;
+  }
   const double teams_us =
       8 + (2 * int64_t(B) > teams ? 4 : 0) + double(items) * Sk * (128 + (Dv <= 64 ? 64 : 128)) * 2 / 5.4e6;
   if (Sk <= 256 || items >= 4 * slots || 1.15 * direct_us < teams_us) return p;
+  p.cluster = 1;
   p.teams = int(std::min<int64_t>(teams, (int64_t(B) * ((int64_t(Sk) + 63) / 64) + 1) / 2));
   const uint64_t parts = uint64_t(B + p.teams) * Hk * R * 2;
   p.off_o = round256(parts * sizeof(float2));
@@ -171,10 +180,12 @@ RowsPlan rows_plan(int B, int H, int Hk, int Sq, int Sk, int Dv) {
 template <int DV, bool BF16>
 int launch_diff_rows(const fa_diff_fwd_params* p, const RowsPlan& plan, cudaStream_t stream) {
   using L = fa::DiffRowsLayout<DV>;
-  static bool done[kMaxDevices] = {}, done_join[kMaxDevices] = {};
-  auto* kern = &fa::fa_diff_rows_kernel<DV, BF16>;
+  static bool done[kMaxDevices] = {}, done_cluster[kMaxDevices] = {}, done_join[kMaxDevices] = {};
+  auto* alone = &fa::fa_diff_rows_kernel<DV, BF16, false>;
+  auto* cluster = &fa::fa_diff_rows_kernel<DV, BF16, true>;
+  auto* kern = plan.cluster > 1 ? cluster : alone;
   auto* join = &fa::fa_diff_rows_join<DV, BF16>;
-  int st = prepare(kern, L::SMEM_ALLOC, done);
+  int st = plan.cluster > 1 ? prepare(cluster, L::SMEM_ALLOC, done_cluster) : prepare(alone, L::SMEM_ALLOC, done);
   if (st != FA_OK || (st = prepare(join, 0, done_join)) != FA_OK) return st;
   CUtensorMap mk[2], mv;
   for (int c = 0; c < 2; ++c)
@@ -203,14 +214,25 @@ int launch_diff_rows(const fa_diff_fwd_params* p, const RowsPlan& plan, cudaStre
   a.R = p->H / p->Hk * p->Sq;
   a.n_mt = (a.R + 15) / 16;
   a.teams = plan.teams;
+  a.cluster = plan.cluster;
   if (plan.teams > 0) {
     if (p->workspace == nullptr || p->workspace_bytes < plan.bytes) return FA_ERR_WORKSPACE;
     a.part_ml = static_cast<float2*>(p->workspace);
     a.part_o = reinterpret_cast<float*>(static_cast<char*>(p->workspace) + plan.off_o);
   }
-  const unsigned grid = unsigned(int64_t(plan.teams > 0 ? plan.teams : p->B) * p->Hk * a.n_mt);
-  kern<<<grid, 256, L::SMEM_ALLOC, stream>>>(mk[0], mk[1], mv, a);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  const unsigned grid = unsigned(int64_t(plan.teams > 0 ? plan.teams : p->B) * p->Hk * a.n_mt * plan.cluster);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = plan.cluster, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = L::SMEM_ALLOC;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = plan.cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, mk[0], mk[1], mv, a) != cudaSuccess) return FA_ERR_CUDA;
   if (plan.teams > 0) {
     return launch_after(join, dim3(unsigned(int64_t(p->B) * p->Hk * a.R)), 256, 0, stream, a);
   }

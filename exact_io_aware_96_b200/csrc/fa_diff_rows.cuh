@@ -19,8 +19,10 @@
 // second small kernel (fa_diff_rows_join), both by the online softmax's
 // rescaling. Two CTAs share an SM, so one's start and end overlap the other's
 // stream. Calls of many batch entries and heads, or of short caches, need no
-// second kernel: one CTA takes all keys of its entry and writes the result
-// ("direct").
+// second kernel ("direct"): one CTA takes all keys of its entry and writes the
+// result, or a cluster of 2, 4 or 8 does. Each of its CTAs then takes a run of
+// units, leaves its piece in its shared memory, and adds up a share of the row
+// tile over all of the cluster's pieces.
 //
 // P is split into two 16-bit terms, p = hi + lo, and multiplied with V twice:
 // the tensor cores have time to spare here, and O keeps the fp32 accuracy of P.
@@ -54,6 +56,7 @@ struct DiffRowsArgs {
   int causal;
   int R, n_mt;   // query rows of a key head, ceil(R / 16)
   int teams;     // 0: direct
+  int cluster;   // direct: CTAs that share an entry's keys (1, 2, 4 or 8)
   // A piece (batch entry b, team t) has slot b + t: along the line one of the two
   // grows from piece to piece.
   float* part_o;    // [slot][hk, row][2][DV]: a piece's unnormalised O_c
@@ -108,8 +111,12 @@ struct DiffRowsLayout {
   // The join's partial results [warp][map][16][DV + 4] reuse the ring.
   static constexpr int OROW = DV + 4;
   static constexpr int JOIN = 4 * 2 * 16 * OROW * 4;
+  // A clustered CTA's piece [map][16][DV], behind it.
+  static constexpr int OFF_PIECE = JOIN;
+  static_assert(OFF_PIECE + 2 * 16 * DV * 4 <= RING, "the piece lies in the ring");
   static constexpr int OFF_ML = RING > JOIN ? RING : JOIN;  // [warp][map][16] (m, l)
-  static constexpr int OFF_BAR = OFF_ML + 4 * 2 * 16 * 8;  // full, empty [stream][stage]
+  static constexpr int OFF_PML = OFF_ML + 4 * 2 * 16 * 8;  // the piece's [map][16] (m, l)
+  static constexpr int OFF_BAR = OFF_PML + 2 * 16 * 8;  // full, empty [stream][stage]
   static constexpr int OFF_MISC = OFF_BAR + 2 * 4 * NS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM_ALLOC = BYTES + 1024;
@@ -141,6 +148,35 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The cluster's barrier in two halves, and its shared memory.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_at(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // What a finished row writes: O, O_2 and both LSEs from both maps' sums.
 // x1, x2: N unnormalised columns from `col` on.
 template <int N, bool BF16, typename Args>
@@ -165,7 +201,7 @@ __device__ __forceinline__ void diff_row_out(const Args& a, int b, int h, int ro
   }
 }
 
-template <int DV, bool BF16>
+template <int DV, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(256, 2)
     fa_diff_rows_kernel(const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmK2,
                         const __grid_constant__ CUtensorMap tmV, const DiffRowsArgs a) {
@@ -181,11 +217,13 @@ __global__ void __launch_bounds__(256, 2)
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;  // fragment row group and column pair
 
-  const int mt = static_cast<int>(blockIdx.x) % a.n_mt;
-  const int hk = static_cast<int>(blockIdx.x) / a.n_mt % a.Hk;
-  const int team = static_cast<int>(blockIdx.x) / a.n_mt / a.Hk;  // direct: the batch entry
+  const int T = CLUSTER ? a.cluster : 1, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  const int item = CLUSTER ? static_cast<int>(blockIdx.x) / T : static_cast<int>(blockIdx.x);
+  const int mt = item % a.n_mt;
+  const int hk = item / a.n_mt % a.Hk;
+  const int team = item / a.n_mt / a.Hk;  // direct: the batch entry
   const int group = a.H / a.Hk;
-  const bool direct = a.teams == 0;
+  const bool direct = CLUSTER || a.teams == 0;
   // The stretch of the line: units [at, end), `before` the units of entries before b.
   int b = team;
   int64_t at = 0, end = 1, before = 0;
@@ -222,8 +260,12 @@ __global__ void __launch_bounds__(256, 2)
   while (at < end) {
     const int len = diff_keys(a.k_lens, b, a.Sk);
     const int64_t units = (len + 63) / 64;
-    const int lo = direct ? 0 : static_cast<int>(at - before) * 64;
-    const int hi = direct ? len : static_cast<int>(min(static_cast<int64_t>(len), (end - before) * 64));
+    const int lo = CLUSTER  ? static_cast<int>(units * rank / T) * 64
+                   : direct ? 0
+                            : static_cast<int>(at - before) * 64;
+    const int hi = CLUSTER  ? min(len, static_cast<int>(units * (rank + 1) / T) * 64)
+                   : direct ? len
+                            : static_cast<int>(min(static_cast<int64_t>(len), (end - before) * 64));
     const int tiles = hi > lo ? (hi - lo + KT - 1) / KT : 0;
     const int mine = tiles > stream ? (tiles - stream + 3) / 4 : 0;  // this stream's tiles: stream, stream + 4, ...
     checked(b < a.B && mt * 16 < a.R, 601);
@@ -353,7 +395,7 @@ __global__ void __launch_bounds__(256, 2)
     used += mine;
     __syncwarp();
     __syncthreads();  // every warp has read its last tile: the ring becomes the join's buffer
-    if (*abort_flag) return;
+    if (!CLUSTER && *abort_flag) return;  // a cluster meets below all the same
 
     float* jo = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -396,7 +438,14 @@ __global__ void __launch_bounds__(256, 2)
         }
       }
       const int row = r % a.Sq, h = hk * group + r / a.Sq;
-      if (direct) {
+      if constexpr (CLUSTER) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          *reinterpret_cast<float4*>(smem + L::OFF_PIECE + ((c * 16 + tr) * DV + col) * 4) =
+              make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+          if (col == 0) reinterpret_cast<float2*>(smem + L::OFF_PML)[c * 16 + tr] = make_float2(mm[c], ll[c]);
+        }
+      } else if (direct) {
         const bool has = len > 0 && (!a.causal || row + len - a.Sq >= 0);
         diff_row_out<4, BF16>(a, b, h, row, col, has, o[0], o[1], ll[0], ll[1]);
         if (col == 0)
@@ -414,6 +463,45 @@ __global__ void __launch_bounds__(256, 2)
           if (col == 0) a.part_ml[slot * 2 + c] = make_float2(mm[c], ll[c]);
         }
       }
+    }
+    if constexpr (CLUSTER) {
+      // The cluster's CTAs hold an entry's keys between them: each adds up a
+      // share of the row tile over all their pieces, out of shared memory.
+      cluster_meet();
+      const uint32_t piece = smem_u32(smem + L::OFF_PIECE), pml = smem_u32(smem + L::OFF_PML);
+      for (int x = threadIdx.x + 256 * rank; x < 16 * (DV / 4); x += 256 * T) {
+        const int tr = x / (DV / 4), col = x % (DV / 4) * 4;
+        const int r = mt * 16 + tr;
+        if (r >= a.R) break;
+        float o[2][4], mm[2], ll[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          mm[c] = -INFINITY;
+          for (int w = 0; w < T; ++w) mm[c] = fmaxf(mm[c], cluster_ld2(cluster_at(pml + (c * 16 + tr) * 8, w)).x);
+          ll[c] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+          for (int w = 0; w < T; ++w) {
+            const float2 v = cluster_ld2(cluster_at(pml + (c * 16 + tr) * 8, w));
+            const float k = v.x == -INFINITY ? (v.y == v.y ? 0.f : v.y) : ex2(v.x - mm[c]);
+            ll[c] += v.y * k;
+            const float4 y = cluster_ld4(cluster_at(piece + ((c * 16 + tr) * DV + col) * 4, w));
+            o[c][0] = fmaf(y.x, k, o[c][0]);
+            o[c][1] = fmaf(y.y, k, o[c][1]);
+            o[c][2] = fmaf(y.z, k, o[c][2]);
+            o[c][3] = fmaf(y.w, k, o[c][3]);
+          }
+        }
+        const int row = r % a.Sq, h = hk * group + r / a.Sq;
+        const bool has = len > 0 && (!a.causal || row + len - a.Sq >= 0);
+        diff_row_out<4, BF16>(a, b, h, row, col, has, o[0], o[1], ll[0], ll[1]);
+        if (col == 0)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            a.lse[((static_cast<int64_t>(c) * a.B + b) * a.H + h) * a.Sq + row] =
+                has ? (mm[c] + __log2f(ll[c])) * 0.69314718055994531f : -INFINITY;
+      }
+      cluster_meet();  // no CTA leaves while another reads its piece
     }
     // On to the next batch entry of the stretch.
     at = before + units;

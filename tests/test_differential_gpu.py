@@ -202,6 +202,37 @@ def test_key_lengths(fa_lib, Sq, Sk, causal):
     within("o2", o2, want["o2"], want["o2_bound"])
 
 
+@pytest.mark.parametrize("Dv", [64, 128])
+@pytest.mark.parametrize("Sq,H,Hk", [(1, 8, 8), (3, 4, 2), (16, 4, 1)])
+@pytest.mark.parametrize("Sk", [128, 300, 640, 1000])
+def test_entries_shared_by_a_cluster(fa_lib, Sk, Sq, H, Hk, Dv):
+    """Caches whose keys 1, 2, 4 or 8 CTAs take together: lengths that leave some of
+    them, or all, without a key, and lengths that end inside a unit of 64. The
+    same call in a graph, replayed, gives the same bits."""
+    lens = [0, 1, 63, 64, 65, Sk - 1, Sk]
+    B, D, dtype = len(lens), 64, torch.float16
+    u, t = ROUND[dtype]
+    q, k, v, lam, _ = case(B, Sq, Sk, H, Hk, D, Dv, dtype, 41 + Sk, "head", torch.float32)
+    want = differential(np64(q), np64(k), np64(v), np64(lam), D ** -0.5, True, n_keys=lens, u=u, t=t)
+    for b, n in enumerate(lens):
+        k[b, n:], v[b, n:] = float("nan"), float("inf")
+    x = [y.cuda() for y in (q, k, v, lam)]
+    kw = dict(causal=True, need_o2=True, k_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    o, lse, o2 = fa.diff_forward(*x, **kw)
+    status_clear()
+    check_lse(lse, want["lse"])
+    within("o", o, want["o"], want["o_bound"])
+    within("o2", o2, want["o2"], want["o2_bound"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = fa.diff_forward(*x, **kw)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    status_clear()
+    assert all(torch.equal(g, w) for g, w in zip(again, (o, lse, o2)))
+
+
 ROWS = [  # B, Sq, Sk, H, Hk, D, Dv, dtype, causal: few rows over many keys
     (1, 1, 16, 1, 1, 64, 128, torch.bfloat16, False),
     (1, 1, 129, 8, 8, 64, 128, torch.float16, True),
