@@ -393,12 +393,12 @@ __global__ void __launch_bounds__(576, 1)
             for (int i = 0; i < 16; ++i)
               if (fwd_pair_on_fma(i)) mx = max3(mx, __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
           }
-          fwd_exp32<BF16, M>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
+          fwd_exp32<BF16, M, true>(sv, 32 * q, lim, sl2x2, negmu2, acc0, acc1, pw[q]);
         }
         float a0, a1;
         f2_split(add2(acc0, acc1), a0, a1);
         add = a0 + a1;
-        return m != -INFINITY && !(add > 256.f) && !(mx * sl2 > m + 8.f);
+        return m != -INFINITY && fabsf(add) <= 256.f && !(mx * sl2 > m + 8.f);
       };
       bool keep = false;  // the first block has no maximum to go ahead with
       if (ready && j > 0) {
@@ -409,9 +409,10 @@ __global__ void __launch_bounds__(576, 1)
       // ahead with the old one, and the two warps meet afterwards, when neither
       // has to wait long. While a half's sum is at most 256, each of its P is: no
       // row maximum is needed to know that the old one will do. (A pair on the
-      // FMA pipe may be anything past 2^128; its scores are looked at.) If a row
-      // of either half asks for a raise, the block's maximum is taken, O_t is
-      // rescaled and the pass is made again.
+      // FMA pipe may be anything past 2^128; its scores are looked at. A NaN there
+      // makes the sum huge, one elsewhere makes it NaN.) If a row of either half
+      // asks for a raise, the block's maximum is taken, O_t is rescaled and the
+      // pass is made again, on the MUFU unit alone, which keeps a NaN.
       tc_fence_before();
       if (!named_bar_and(pair_bar, 64, keep)) {
         const bool in = ready && __all_sync(0xffffffffu, wait_bar(&s_full[2 * t + 1], j & 1, abort_flag, kRoleSoftmax, j));

@@ -109,7 +109,7 @@ struct FwdLayout {
 // runs on the MUFU unit, which returns exactly 0 for them.
 // Which of the pairs go to the FMA pipe where nothing is masked.
 __device__ constexpr bool fwd_pair_on_fma(int cc) { return (cc & 3) == 3; }
-template <bool BF16, bool MASKED>
+template <bool BF16, bool MASKED, bool KEEP_NAN = false>
 __device__ __forceinline__ void fwd_exp32(const uint32_t (&sv)[32], int col0, int lim, uint64_t sl2x2,
                                           uint64_t negmu2, uint64_t& acc0, uint64_t& acc1, uint32_t (&pw)[16]) {
   using namespace sm100;
@@ -124,7 +124,7 @@ __device__ __forceinline__ void fwd_exp32(const uint32_t (&sv)[32], int col0, in
     const uint64_t tt = fma2(f2(s0, s1), sl2x2, negmu2);
     uint64_t e;
     if (!MASKED && fwd_pair_on_fma(cc)) {
-      e = exp2_poly2(tt);
+      e = exp2_poly2<KEEP_NAN>(tt);
     } else {
       float t0, t1;
       f2_split(tt, t0, t1);

@@ -466,12 +466,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // [-1/2, 1/2] (fit_exp2_poly.py beside this file; max relative error 7.5e-5),
 // and 2^n added into the exponent field. t is clamped below at -126, so
 // arguments under it (including -inf) give a value below 2^-125, not 0:
-// callers that need exact zeros must not rely on this path for them.
+// callers that need exact zeros must not rely on this path for them. The clamp
+// also drops a NaN, which then gives 2^-126; with KEEP_NAN it does not, and a
+// NaN gives what its bits are after the addition into the exponent field: the
+// canonical NaN's, 0x7fffffff + (0x7fffffff << 23), the largest float.
+template <bool KEEP_NAN = false>
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t t) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer in the low mantissa bits
   float t0, t1;
   f2_split(t, t0, t1);
-  t = f2(fmaxf(t0, -126.f), fmaxf(t1, -126.f));
+  if constexpr (KEEP_NAN) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(t0) : "f"(-126.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(t1) : "f"(-126.f));
+    t = f2(t0, t1);
+  } else {
+    t = f2(fmaxf(t0, -126.f), fmaxf(t1, -126.f));
+  }
   const uint64_t r = add2(t, f2(kMagic, kMagic));
   const uint64_t n = add2(r, f2(-kMagic, -kMagic));
   const uint64_t f = fma2(n, f2(-1.f, -1.f), t);
