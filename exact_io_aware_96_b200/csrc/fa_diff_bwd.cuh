@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(256) fa_diff_pre(const DiffBwdArgs a) {
         l1 = e1 * 1.4426950408889634f;
         l2 = e2 * 1.4426950408889634f;
         lam = load_lam(a.lam, a.lam_kind, b * a.lam_s[0] + i * a.lam_s[1] + h * a.lam_s[2]);
+        // A NaN logsumexp has to reach every -lambda P_2 of the row: the exponentials
+        // on the FMA pipe drop it, this factor does not.
+        if (e2 != e2) lam = e2;
       } else {
         d_o = d_2 = 0.f;
       }

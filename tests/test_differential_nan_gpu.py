@@ -73,3 +73,32 @@ def test_a_score_of_minus_infinity_is_a_masked_key(fa_lib, dtype):
         check_lse(lse, want["lse"])
         within("o", o, want["o"], want["o_bound"])
         within("o2", o2, want["o2"], want["o2_bound"])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("Sq,causal", [(160, False), (512, True)])
+def test_backward(fa_lib, Sq, causal, dtype):
+    """The NaN reaches dv and the NaN map's dk at every key that such a row sees, its dq
+    in every such row, dlambda where it is in map 2. Rows that do not see it keep their
+    dlambda, and their dq where no block of theirs holds the key (0 x NaN is NaN)."""
+    Sk = 512
+    q, k, v, lam, do, at = planted(Sq, Sk, float("nan"), dtype)
+    want = oracle_without(q, k, v, lam, do, causal, dtype)
+    cu = [x.cuda() for x in (q, k, v, lam, do)]
+    o, lse, o2 = fa.diff_forward(*cu[:4], causal=causal, scale=1.0, need_o2=True)
+    dq, dk, dv, dlam = (np64(x) for x in fa.diff_backward(*cu[:4], o, o2, lse, cu[4], causal=causal, scale=1.0))
+    status_clear()
+    B, H = at.shape
+    rows = (np.arange(Sq)[None, :, None] + (Sk - Sq if causal else Sk)) >= at[:, None, :]  # [B, Sq, H]
+    # Every key is seen by a NaN row: the last row sees them all.
+    assert rows[:, -1].all() and np.isnan(dv).all()
+    for c in (0, 1):
+        mine = np.arange(B) % 2 == c
+        assert np.isnan(dk[mine][:, :, :, c, 0]).all()  # dS is NaN; q's first column is 1
+        hit = rows & mine[:, None, None]
+        assert np.isnan(dq[:, :, :, c][hit]).all()
+    assert np.isnan(dlam[rows & (np.arange(B) % 2 == 1)[:, None, None]]).all()
+    for name, got, ok in (("dq", dq, ~rows & (np.arange(Sq) < BLOCK)[None, :, None]), ("dlam", dlam, ~rows)):
+        w, bd = want[name][ok], want[name + "_bound"][ok]
+        u, t = ROUND[dtype]
+        within(name, torch.from_numpy(got[ok]), w, bd + u * np.abs(w) + t)
