@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <optional>
@@ -231,14 +232,36 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor> diff_backward(
   return {status, dq, dk, dv, dlam};
 }
 
-// [B, S, heads, D], or [B, S, H, 2, D] with the two maps as neighbouring heads.
-Tensor heads_of(const char* name, const Tensor& t) {
+// What one launch turns: a [B, S, heads, D] view and where it goes.
+struct Turn {
+  Tensor in, out;
+};
+
+void check_heads(const char* name, const Tensor& t) {
   TORCH_CHECK_VALUE(t.dim() == 4 || t.dim() == 5, name, " must be [B, S, heads, D] or [B, S, H, 2, D]");
+}
+
+// Whether the head and map axes of a [B, S, H, 2, D] tensor are one run of heads.
+bool one_run(const Tensor& t) {
+  return t.dim() == 4 || t.size(2) <= 1 || t.stride(2) == t.size(3) * t.stride(3);
+}
+
+Tensor joined(const Tensor& t) {
   if (t.dim() == 4) return t;
-  TORCH_CHECK_VALUE(t.size(2) <= 1 || t.stride(2) == t.size(3) * t.stride(3), name,
-                    ": the head axes of [B, S, H, 2, D] must be one run of heads");
   return t.as_strided({t.size(0), t.size(1), t.size(2) * t.size(3), t.size(4)},
                       {t.stride(0), t.stride(1), t.stride(3), t.stride(4)});
+}
+
+// [B, S, heads, D] in one piece, [B, S, H, 2, D] with its maps as neighbouring
+// heads, or map by map where the strides of either side do not allow that.
+std::vector<Turn> turns_of(const char* name, const Tensor& in, const Tensor& out) {
+  if (one_run(in) && one_run(out)) return {{joined(in), joined(out)}};
+  // (What the library finds wrong with one map's views it finds with the first's.)
+  TORCH_CHECK_VALUE(in.stride(3) % 8 == 0 && out.stride(3) % 8 == 0, name,
+                    ": the strides must be multiples of 8 elements");
+  std::vector<Turn> turns;
+  for (int64_t c = 0; c < in.size(3); ++c) turns.push_back({in.select(3, c), out.select(3, c)});
+  return turns;
 }
 
 std::tuple<int, Tensor, OptTensor> rotary(const Tensor& q, const OptTensor& k, const Tensor& positions,
@@ -248,12 +271,13 @@ std::tuple<int, Tensor, OptTensor> rotary(const Tensor& q, const OptTensor& k, c
   fa_rotary_params p{};
   p.dtype = dtype_code(q);
   need_cuda(q);
-  const Tensor hq = heads_of("q", q);
-  const int64_t B = hq.size(0), S = hq.size(1), D = hq.size(3);
-  Tensor hk;
+  check_heads("q", q);
+  const int64_t B = q.size(0), S = q.size(1), D = q.size(-1);
   if (k) {
-    hk = heads_of("k", *k);
-    expect("k", hk, {B, S, hk.size(2), D}, q.scalar_type(), q);
+    check_heads("k", *k);
+    std::vector<int64_t> shape = k->sizes().vec();
+    shape[0] = B, shape[1] = S, shape.back() = D;
+    expect("k", *k, shape, q.scalar_type(), q);
   }
   TORCH_CHECK_VALUE(positions.dim() == 2 || positions.dim() == 3, "positions: expected [axes, B, S] or [B, S]");
   const Tensor pos = positions.dim() == 2 ? positions.unsqueeze(0) : positions;
@@ -286,23 +310,33 @@ std::tuple<int, Tensor, OptTensor> rotary(const Tensor& q, const OptTensor& k, c
   Tensor out_q = out_q_ ? *out_q_ : at::empty(q.sizes(), q.options());
   OptTensor out_k = out_k_;
   if (k && !out_k) out_k = at::empty(k->sizes(), q.options());
-  p.q = flat("q", hq);
-  p.q_out = flat("out_q", heads_of("out_q", out_q));
-  if (k) {
-    p.k = flat("k", hk);
-    p.k_out = flat("out_k", heads_of("out_k", *out_k));
-    p.Hk = as_int(hk.size(2));
-  }
+  const std::vector<Turn> qs = turns_of("q", q, out_q);
+  const std::vector<Turn> ks = k ? turns_of("k", *k, *out_k) : std::vector<Turn>();
   p.positions = pos.data_ptr();
   p.pos_stride_axis = pos.stride(0), p.pos_stride_b = pos.stride(1), p.pos_stride_s = pos.stride(2);
   p.pos_int64 = pos.scalar_type() == at::kLong;
   p.inv_freq = inv_freq.data_ptr();
   p.inv_freq_fp64 = inv_freq.scalar_type() == at::kDouble;
   p.axes = as_int(axes);
-  p.B = as_int(B), p.S = as_int(S), p.H = as_int(hq.size(2)), p.D = as_int(D);
+  p.B = as_int(B), p.S = as_int(S), p.D = as_int(D);
   p.interleaved = interleaved;
   p.inverse = inverse;
-  const int status = api.rotary(&p, stream_of(q));
+  // One launch, unless maps lie apart. The first one checks every view but for
+  // the further maps' places, so that a refused call writes nothing.
+  int status = FA_OK;
+  for (size_t i = 0; i < std::max(qs.size(), ks.size()) && status == FA_OK; ++i) {
+    const Turn& t = i < qs.size() ? qs[i] : ks[i];
+    p.q = flat("q", t.in);
+    p.q_out = flat("out_q", t.out);
+    p.H = as_int(t.in.size(2));
+    p.Hk = 0;
+    if (i < qs.size() && i < ks.size()) {
+      p.k = flat("k", ks[i].in);
+      p.k_out = flat("out_k", ks[i].out);
+      p.Hk = as_int(ks[i].in.size(2));
+    }
+    status = api.rotary(&p, stream_of(q));
+  }
   return {status, out_q, out_k};
 }
 
