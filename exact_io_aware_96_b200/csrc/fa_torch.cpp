@@ -111,6 +111,18 @@ Sizes sizes_of(const Tensor& q, const Tensor& k, const Tensor& v) {
   return s;
 }
 
+// A tensor that the caller gives as an output: no gradient can flow through the
+// write, so it is refused where autograd would record one...
+void writable(const char* name, const OptTensor& t) {
+  TORCH_CHECK_VALUE(!t || !t->requires_grad() || !at::GradMode::is_enabled(), name,
+                    ": an output that requires a gradient (use the functions of autograd.py, or torch.no_grad)");
+}
+// ...and its version goes up, so that a backward pass that has saved it finds out.
+void written(std::initializer_list<const OptTensor*> outputs) {
+  for (const OptTensor* t : outputs)
+    if (*t && !(*t)->is_inference()) (*t)->unsafeGetTensorImpl()->bump_version();
+}
+
 fa_diff_lambda lambda_of(const Tensor& lam, const Sizes& s, const Tensor& q) {
   TORCH_CHECK_VALUE(lam.dim() <= 3, "lam must be a tensor that broadcasts to [B, Sq, H]");
   const int full[3] = {s.B, s.Sq, s.H};
@@ -156,6 +168,9 @@ std::tuple<int, Tensor, Tensor, OptTensor> diff_forward(const Tensor& q, const T
                                                         const OptTensor& k_lens, bool need_o2, const OptTensor& out_,
                                                         const OptTensor& out2_, const OptTensor& lse_,
                                                         const OptTensor& workspace) {
+  writable("out", out_);
+  writable("out2", out2_);
+  writable("lse", lse_);
   const Sizes s = sizes_of(q, k, v);
   fa_diff_fwd_params p{};
   p.lambda = lambda_of(lam, s, q);
@@ -187,6 +202,7 @@ std::tuple<int, Tensor, Tensor, OptTensor> diff_forward(const Tensor& q, const T
   const size_t bytes = workspace || s.Sq > 16 ? 0 : api.fwd_ws(s.B, s.H, s.Hk, s.Sq, s.Sk, s.D, s.Dv, causal);
   set_workspace(p, hold, workspace, bytes, q);
   const int status = api.fwd(&p, stream_of(q));
+  if (status == FA_OK) written({&out_, &out2_, &lse_});
   return {status, out, lse, out2};
 }
 
@@ -194,6 +210,10 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor> diff_backward(
     const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& lam, const Tensor& o, const Tensor& o2,
     const Tensor& lse, const Tensor& dO, bool causal, std::optional<double> scale, const OptTensor& dq_,
     const OptTensor& dk_, const OptTensor& dv_, const OptTensor& dlam_, const OptTensor& workspace, bool deterministic) {
+  writable("dq", dq_);
+  writable("dk", dk_);
+  writable("dv", dv_);
+  writable("dlam", dlam_);
   const Sizes s = sizes_of(q, k, v);
   fa_diff_bwd_params p{};
   p.lambda = lambda_of(lam, s, q);
@@ -229,6 +249,7 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor> diff_backward(
   const size_t bytes = workspace ? 0 : api.bwd_ws(s.B, s.H, s.Hk, s.Sq, s.Sk, s.D, s.Dv, causal, deterministic);
   set_workspace(p, hold, workspace, bytes, q);
   const int status = api.bwd(&p, stream_of(q));
+  if (status == FA_OK) written({&dq_, &dk_, &dv_, &dlam_});
   return {status, dq, dk, dv, dlam};
 }
 
@@ -268,6 +289,8 @@ std::tuple<int, Tensor, OptTensor> rotary(const Tensor& q, const OptTensor& k, c
                                           const Tensor& inv_freq, const std::optional<std::vector<int64_t>>& sections,
                                           bool interleaved, bool inverse, const OptTensor& out_q_,
                                           const OptTensor& out_k_) {
+  writable("out_q", out_q_);
+  writable("out_k", out_k_);
   fa_rotary_params p{};
   p.dtype = dtype_code(q);
   need_cuda(q);
@@ -337,6 +360,7 @@ std::tuple<int, Tensor, OptTensor> rotary(const Tensor& q, const OptTensor& k, c
     }
     status = api.rotary(&p, stream_of(q));
   }
+  if (status == FA_OK) written({&out_q_, &out_k_});
   return {status, out_q, out_k};
 }
 
