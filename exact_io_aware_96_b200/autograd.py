@@ -104,6 +104,6 @@ def diff_attn_func(q, k, v, lam, causal: bool = False, softmax_scale=None, deter
 
 
 def rotary_func(q, k, positions, inv_freq, sections=None, interleaved: bool = False):
-    """(q, k) with rotary positions of one or more axes applied, differentiable (once) in q and k (k may be None);
-    see ``fa.rotary``."""
+    """(q, k) with rotary positions of one or more axes applied, differentiable (once) in q and k (k may be None),
+    not in inv_freq, which is refused if it requires a gradient; see ``fa.rotary``."""
     return fa.native().rotary_attached(q, k, positions, inv_freq, sections, interleaved)

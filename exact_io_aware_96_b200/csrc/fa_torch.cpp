@@ -472,6 +472,7 @@ struct Rotary : torch::autograd::Function<Rotary> {
 std::tuple<Tensor, OptTensor> rotary_attached(const Tensor& q, const OptTensor& k, const Tensor& positions,
                                               const Tensor& inv_freq,
                                               const std::optional<std::vector<int64_t>>& sections, bool interleaved) {
+  TORCH_CHECK_VALUE(!recorded({&inv_freq}), "inv_freq requires a gradient: there is none in the frequencies");
   auto out = Rotary::apply(q, k, positions, inv_freq, sections, interleaved);
   return {out[0], out.size() > 1 ? OptTensor(out[1]) : OptTensor()};
 }

@@ -593,7 +593,8 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=
     inv_freq fp32 or fp64 [R]; sections gives the pairs of each axis (default:
     all on the only axis). Pairs are columns (j, j + R), or (2j, 2j + 1) if
     interleaved; columns from 2R on are copied. inverse turns back: it is also
-    the gradient. out_q may be q and out_k may be k (in place)."""
+    the gradient. out_q may be q and out_k may be k (in place). No gradient is
+    recorded: outputs that require one are refused (autograd.rotary_func)."""
     if _elsewhere(q, stream):
         with _on(q.device, stream):
             return rotary(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k)

@@ -1,8 +1,9 @@
-"""Refusals of outputs that autograd would lose track of, found before any CUDA call."""
+"""Refusals of outputs and inputs that autograd would lose track of, found before any CUDA call."""
 import pytest
 import torch
 
 from exact_io_aware_96_b200 import fa
+from exact_io_aware_96_b200.autograd import rotary_func
 
 
 def half(*s):
@@ -21,3 +22,9 @@ def test_outputs_that_require_a_gradient(fa_lib):
     for name, t in dict(dq=q, dk=q, dv=v, dlam=lam).items():
         with pytest.raises(ValueError, match="gradient"):
             fa.diff_backward(q, q, v, lam, v, v, torch.zeros(2, 1, 2, 4), v, **{name: t.clone().requires_grad_()})
+
+
+def test_frequencies_get_no_gradient(fa_lib):
+    x, pos, f = half(1, 4, 2, 64), torch.zeros(1, 1, 4, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="inv_freq"):
+        rotary_func(x, None, pos, f.requires_grad_())

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from exact_io_aware_96_b200 import fa
+from exact_io_aware_96_b200.autograd import rotary_func
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +93,12 @@ def test_outputs_of_inference_mode(fa_lib):
         assert torch.equal(x, want)
     fa.rotary(half(1, 9, 2, 64), None, pos, f, out_q=x)  # outside of it too: no version to raise
     assert fa.fa_last_device_status()[0] == 0
+
+
+def test_frequencies_get_no_gradient(fa_lib):
+    pos, f = positions(9)
+    x = half(1, 9, 2, 64).requires_grad_()
+    with pytest.raises(ValueError, match="inv_freq"):
+        rotary_func(x, None, pos, f.requires_grad_())
+    with torch.no_grad():
+        assert torch.equal(rotary_func(x, None, pos, f)[0], fa.rotary(x.detach(), None, pos, f.detach())[0])
