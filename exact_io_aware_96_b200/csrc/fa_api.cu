@@ -37,6 +37,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// Whether the calling thread has a current context.
+bool context_current() {
+  static PFN_cuCtxGetCurrent_v4000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
+  });
+  CUcontext ctx = nullptr;
+  return fn && fn(&ctx) == CUDA_SUCCESS && ctx != nullptr;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Checks shared by every tensor view of a call.
@@ -121,10 +136,11 @@ int prepare(F* fn, int smem_bytes, bool (&done)[kMaxDevices]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
-  // Binds the device's primary context to this thread: a thread that has made
-  // no other CUDA call yet (an autograd worker whose buffers came from a cache)
-  // has none, and cuTensorMapEncodeTiled, a driver call, needs one.
-  if (cudaSetDevice(dev) != cudaSuccess) return FA_ERR_CUDA;
+  // A thread that has made no other CUDA call yet (an autograd worker whose
+  // buffers came from a cache) has no context, and cuTensorMapEncodeTiled, a
+  // driver call, needs one: the device's primary context is bound. A context
+  // that is current stays so: it may be the caller's own (cuCtxCreate).
+  if (!context_current() && cudaSetDevice(dev) != cudaSuccess) return FA_ERR_CUDA;
   if (!done[dev]) {
     if (smem_bytes > 0 &&
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
