@@ -739,7 +739,7 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
 
 int fa_selftest_wait_timeout(unsigned int limit_us, fa_stream_t stream) {
   if (limit_us < 1 || limit_us > 4000000u) return FA_ERR_INVALID_ARG;
-  fa::fa_selftest_wait_kernel<<<1, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(uint64_t(limit_us) * 1000u);
+  fa::fa_selftest_wait_kernel<<<1, 96, 0, reinterpret_cast<cudaStream_t>(stream)>>>(uint64_t(limit_us) * 1000u);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

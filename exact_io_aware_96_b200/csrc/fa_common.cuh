@@ -85,8 +85,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 // arrives on, with a limit of limit_ns; it records the timeout in the status
 // word and raises the block's abort flag. Warp 1 waits on the same barrier
 // with the normal limit and leaves as soon as it sees the abort flag, the way
-// the other roles of a pipeline wind down.
-__global__ void __launch_bounds__(64) fa_selftest_wait_kernel(uint64_t limit_ns) {
+// the other roles of a pipeline wind down. In warp 2 one lane alone waits, as
+// where one lane feeds a ring for its warp: the warp leaves together, at a vote.
+__global__ void __launch_bounds__(96) fa_selftest_wait_kernel(uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {
@@ -98,8 +99,14 @@ __global__ void __launch_bounds__(64) fa_selftest_wait_kernel(uint64_t limit_ns)
   const int warp = threadIdx.x >> 5;
   if (warp == 0)
     wait_bar(&bar, 0, &abort_flag, kRoleSelfTest, 0, limit_ns);
-  else
+  else if (warp == 1)
     wait_bar(&bar, 0, &abort_flag, kRoleSelfTest, 1);
+  else
+    for (bool fed = true;;) {
+      if (!__all_sync(0xffffffffu, fed)) break;
+      if ((threadIdx.x & 31) == 0) fed = wait_bar(&bar, 0, &abort_flag, kRoleSelfTest, 2);
+      __syncwarp();
+    }
 }
 
 struct FwdArgs {

@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(256, 2)
       for (int vb = 0; vb < L::VB; ++vb) tma_load_4d(dst + (2 + vb) * KT * 128, &tmV, &full[st], vb * 64, key, hk, b);
     };
     const bool loads = c == 0 && lane == 0;
+    bool fed = true;  // false in the loading lane once its wait for a free stage has run out
     int issued = 0;
     if (loads)
       for (; issued < min(NS, mine); ++issued) issue(issued);
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(256, 2)
     for (int i = 0; i < mine; ++i) {
       const int st = (used + i) % NS, key0 = lo + (stream + 4 * i) * KT;
       const uint32_t ph_st = ((used + i) / NS) & 1;
-      if (!__all_sync(0xffffffffu, wait_bar_c(&full[st], ph_st, abort_flag, kRoleSoftmax, i))) break;
+      if (!__all_sync(0xffffffffu, fed && wait_bar_c(&full[st], ph_st, abort_flag, kRoleSoftmax, i))) break;
       uint8_t* tile = ring + st * L::TILE;
       const uint32_t sk = smem_u32(tile) + c * KT * 128, sv = smem_u32(tile) + 2 * KT * 128;
       if (key0 + KT > len) {
@@ -385,9 +386,10 @@ __global__ void __launch_bounds__(256, 2)
       if (lane == 0) mbar_arrive(&empty[st]);
       if (loads && i + NS < mine) {
         // The other map's warp is at most a tile behind in the same stage.
-        if (!wait_bar_c(&empty[st], ph_st, abort_flag, kRoleLoader, i)) break;  // the abort flag is up
-        issue(i + NS);
-        ++issued;
+        // If the wait runs out (the abort flag is then up) the lane does not leave
+        // alone: its warp leaves together at the next tile's vote.
+        fed = wait_bar_c(&empty[st], ph_st, abort_flag, kRoleLoader, i);
+        if (fed) issue(i + NS), ++issued;
       }
     }
     if (loads && *abort_flag)  // let the copies already issued land before the CTA exits
