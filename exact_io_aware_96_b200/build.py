@@ -1,6 +1,8 @@
 """Build libfa.so (the CUDA library) in-tree with nvcc for sm_100a, and
 _fa_torch.so (the torch side of differential attention and rotary positions,
-host code only) with the C++ compiler against the installed torch.
+host code only) with the C++ compiler against the installed torch. libfa.so
+alone needs neither torch nor Python's headers: without them _fa_torch.so is
+left out, with a note on stderr.
 
 Usage: ``python -m exact_io_aware_96_b200.build`` (or ``__graft_entry__.build()``).
 The CUDA runtime is linked statically; the driver API is reached through
@@ -34,6 +36,20 @@ LIB_CHECK = os.path.join(HERE, "libfa_check.so")
 
 TORCH_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
 TORCH_LIB = os.path.join(HERE, "_fa_torch.so")
+
+
+def torch_missing() -> str | None:
+    """What _fa_torch.so cannot be built without and is not here, or None."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    for header in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                   os.path.join(os.path.dirname(torch.__file__), "include", "ATen", "ATen.h")):
+        if not os.path.exists(header):
+            return header
+    return None
 
 
 def build_torch() -> str:
@@ -77,7 +93,11 @@ def build(verbose: bool = False, extra: list[str] | None = None, check: bool = F
     if verbose:
         sys.stdout.write(res.stdout + res.stderr)
     if not check:
-        build_torch()
+        if missing := torch_missing():
+            print(f"_fa_torch.so is not built (differential attention and rotary positions from Python need it): "
+                  f"{missing} is missing", file=sys.stderr)
+        else:
+            build_torch()
     return out
 
 
