@@ -15,8 +15,10 @@ import pytest  # noqa: E402
 
 @pytest.fixture(scope="session")
 def fa_lib():
-    """The built libfa.so (built in-tree first if it is missing)."""
+    """The built libfa.so, with _fa_torch.so beside it (built in-tree first if they are missing)."""
     from exact_io_aware_96_b200 import build, fa
     if not os.path.exists(fa.LIB_PATH):
         build.build()
+    if not os.path.exists(build.TORCH_LIB):
+        build.build_torch()
     return fa.lib()
