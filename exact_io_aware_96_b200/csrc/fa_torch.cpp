@@ -198,8 +198,7 @@ std::tuple<int, Tensor, Tensor, OptTensor> diff_forward(const Tensor& q, const T
   p.causal = causal;
   p.dtype = s.dtype;
   Tensor hold;
-  // Calls of more than 16 rows need none.
-  const size_t bytes = workspace || s.Sq > 16 ? 0 : api.fwd_ws(s.B, s.H, s.Hk, s.Sq, s.Sk, s.D, s.Dv, causal);
+  const size_t bytes = workspace ? 0 : api.fwd_ws(s.B, s.H, s.Hk, s.Sq, s.Sk, s.D, s.Dv, causal);
   set_workspace(p, hold, workspace, bytes, q);
   const int status = api.fwd(&p, stream_of(q));
   if (status == FA_OK) written({&out_, &out2_, &lse_});
