@@ -301,7 +301,7 @@ SplitPlan plan_split(int B, int H, int Sq, int Sk, int Dk, int causal, int split
   return best;
 }
 
-// Distinct for every launch of the split forward (the tickets compare it).
+// Odd, and distinct for every call of the split forward (the tickets compare it).
 unsigned long long next_epoch() {
   static std::atomic<unsigned long long> epoch{
       (uint64_t(std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull) | 1ull};

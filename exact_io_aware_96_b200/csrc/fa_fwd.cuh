@@ -151,7 +151,8 @@ __device__ __forceinline__ void fwd_exp32(const uint32_t (&sv)[32], int col0, in
 // into its workspace slot; the 16 softmax warps meet; one thread fences and
 // swaps the pair's ticket to this launch's epoch; the CTA that finds the
 // epoch already there (the second to finish) fences again and reads its
-// partner's partial through L2, then writes O and LSE. The barrier orders the
+// partner's partial through L2, then writes O and LSE. It also clears the ticket:
+// a captured launch brings the same epoch at every replay. The barrier orders the
 // other threads' partial stores before that thread's fence (fences are
 // cumulative), so one fence per CTA suffices.
 // Partial O layout: float4 units [CTA][tile][D / 4][128 rows], so a warp's
@@ -211,7 +212,10 @@ __device__ __forceinline__ void fwd_split_epilogue(const FwdArgs& a, uint8_t* fl
     if (go && checked(pair < a.n_split * a.H * a.B, 112)) {
       __threadfence();
       second = atomicExch(&a.tickets[pair], a.epoch) == a.epoch;
-      if (second) __threadfence();
+      if (second) {
+        __threadfence();
+        a.tickets[pair] = 0;  // no epoch: those are odd
+      }
     }
     *second_flag = second;
   }
