@@ -23,7 +23,8 @@ enum Role : int { kRoleLoader = 1, kRoleMma = 2, kRoleSoftmax = 3, kRoleSelfTest
 // failed index or bounds test in the status word (FA_ERR_BOUNDS, role 5, the
 // site number in place of the loop index) and returns false, so that the
 // caller skips the access. In the normal build it is `true` and the test is
-// not compiled. Sites: 1xx 16-bit forward, 2xx backward, 3xx e4m3 forward.
+// not compiled. Sites: 1xx 16-bit forward, 2xx backward, 3xx e4m3 forward, 4xx
+// differential forward, 5xx its backward, 6xx its few-row form.
 #ifndef FA_CHECK
 #define FA_CHECK 0
 #endif

@@ -54,11 +54,23 @@
 // dS^T go to dV and dK through tensor memory). The softmax's two phases take
 // about 2300 cycles a chunk and overlap the products except for the hand-offs
 // (W ready -> dV, S ready -> exponentials, dS ready -> dK). Measured at B = 1,
-// H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 455 us, 753 TFLOP/s, tensor
-// pipe 36% active. Without the exponentials the same grid takes 440 us, without
-// the dQ reductions 459 of 474: no single part carries the rest. Tried and
-// slower: 16 softmax warps of 16 columns (550 us), dQ_2 over dP's columns with
-// dK from shared memory (602), dQ by red.global instead of the TMA (604).
+// H = 8, S = 8192, D = 64, DV = 128, bf16, causal, all kernels of the call in
+// bursts at 1965 MHz: 422 us, 814 TFLOP/s, tensor pipe 39% active; 480 when
+// launched for a second without a pause (1700 MHz under the power cap). Of 474 us
+// at an earlier step: without the exponentials 440, without the dQ reductions
+// 459; no single part carries the rest. Tried and slower, against 455 to 490: 16
+// softmax warps of 16 columns (550 us), dQ_2 over dP's columns with dK from shared
+// memory (602), dQ by red.global instead of the TMA (604). At DV = 128 three
+// registers of a thread spill (12 bytes, once each way).
+//
+// Rounded to 16 bits, as operands of the tensor cores: W before dV, dS_c before
+// dQ_c and dK_c. Delta_c and dlambda come from O and O_2, which the forward has
+// rounded to 16 bits (once as P's, once as their own): a sum over P_2 dP in fp32
+// would spare dlambda that, at a row sum over the lanes in every chunk's softmax.
+// Relative errors in norm, bf16 (rounding the result alone: 1.7e-3): dQ and dK
+// 2.5e-3, dV 2.4e-3, dlambda 2.7e-3; fp16 (2.1e-4): 3.0e-4, 2.9e-4, 3.6e-4. An fp32
+// dlambda of every row keeps 2.1e-3 (fp16: 2.9e-4); summed over 4,000 rows and
+// more, one of a head is off by less than 1e-4 of its terms' magnitudes.
 #pragma once
 
 #include <type_traits>

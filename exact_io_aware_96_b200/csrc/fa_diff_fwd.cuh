@@ -24,6 +24,10 @@
 // says that no P is above 2^8. A block that does ask for a raise (the first one
 // always does) has its maximum taken and is passed over again.
 //
+// P_c is rounded to 16 bits as P V's operand (a second 16-bit term, as in the
+// few-row form, would cost a second product). O's relative error in norm is then
+// 2.4e-3 in bf16 and 3.2e-4 in fp16; rounding O alone gives 1.7e-3 and 2.1e-4.
+//
 // Warp roles (576 threads):
 //   warps 8t + 4c + r  softmax of map t, key half c of every block, TMEM lanes
 //              32r .. 32r + 31, one query row per thread
@@ -41,10 +45,13 @@
 // pipe) and 1500 issue slots per scheduler; a block takes about 2700. A map's
 // chain of P V, the second half's S and softmax, and the hand-offs between them
 // (a wake-up is about 300 cycles) overlaps the other map's and the first half's
-// only. Measured at B = 1, H = 8, S = 8192, D = 64, DV = 128, bf16, causal: 198
-// us, 1041 TFLOP/s; 208 with the maximum of every block taken, 212 with the first
-// block's exponentials computed twice, 214 with the first half's next S made when
-// all of P is there, 225 with S in one N = 128 product after P V. Slower: 64-key
+// only. Measured at B = 1, H = 8, S = 8192, D = 64, DV = 128, bf16, causal, in
+// bursts of launches at 1965 MHz: 198 to 203 us on several GPUs, 1015 to 1041
+// TFLOP/s. (Launched for a second without a pause it takes 230 us: the power cap
+// brings the clock to 1700 MHz.) Against 198: 208 with the maximum of every block
+// taken, 212 with the first block's exponentials computed twice, 214 with the
+// first half's next S made when all of P is there, 225 with S in one N = 128
+// product after P V. Slower: 64-key
 // blocks in two buffers per map (356 us), an issuing warp per map (299), the first
 // half's warps taking 80 keys of the 128 (213 against 212), waits out of line (222
 // against 208), P in columns of its own where DV = 64 leaves room (60 against 56),

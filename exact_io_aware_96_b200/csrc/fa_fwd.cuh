@@ -103,12 +103,13 @@ struct FwdLayout {
   static constexpr int TMEM_COLS = 512;
 };
 
+// Which of the pairs go to the FMA pipe where nothing is masked.
+__device__ constexpr bool fwd_pair_on_fma(int cc) { return (cc & 3) == 3; }
 // P = 2^(s * sl2 - mu) for 32 S values of one row (raw fp32 bits in sv),
 // packed to 16 words of two 16-bit values; adds the P values into acc0/acc1.
 // MASKED: entries past column `lim` are -inf (P = 0) and every exponential
-// runs on the MUFU unit, which returns exactly 0 for them.
-// Which of the pairs go to the FMA pipe where nothing is masked.
-__device__ constexpr bool fwd_pair_on_fma(int cc) { return (cc & 3) == 3; }
+// runs on the MUFU unit, which returns exactly 0 for them. KEEP_NAN: see
+// exp2_poly2.
 template <bool BF16, bool MASKED, bool KEEP_NAN = false>
 __device__ __forceinline__ void fwd_exp32(const uint32_t (&sv)[32], int col0, int lim, uint64_t sl2x2,
                                           uint64_t negmu2, uint64_t& acc0, uint64_t& acc1, uint32_t (&pw)[16]) {

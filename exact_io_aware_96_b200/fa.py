@@ -547,7 +547,9 @@ def diff_forward(q, k, v, lam, causal=False, scale=None, k_lens=None, need_o2=Fa
     (float32 or q's dtype) broadcasts to [B, Sq, H]. k_lens, int32 [B]: batch
     entry b attends to its first k_lens[b] keys, and the causal mask aligns to
     that end. LSE is fp32 [2, B, H, Sq]. O2 = softmax(scale q_2 k_2^T) v is
-    written if need_o2 or out2 asks for it (diff_backward needs it), else None."""
+    written if need_o2 or out2 asks for it (diff_backward needs it), else None.
+    No gradient is recorded (autograd.diff_attn_func): given outputs that require
+    one are refused."""
     if _elsewhere(q, stream):
         with _on(q.device, stream):
             return diff_forward(q, k, v, lam, causal, scale, k_lens, need_o2, out, out2, lse, workspace)
@@ -561,8 +563,9 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal=False, scale=None, dq=Non
                   workspace=None, stream=None, deterministic=False):
     """(dQ, dK, dV, dLam) of L = sum(dO * O) for O of diff_forward, whose o, o2
     and lse it takes. dLam has lam's shape and dtype: the gradient is summed
-    over the axes lam is broadcast over. ``deterministic=True`` sums dQ in a
-    fixed order (dK, dV and dLam always are)."""
+    over the axes lam is broadcast over; it comes from o2, so a float32 one has
+    the precision of q's dtype too. ``deterministic=True`` sums dQ in a fixed
+    order (dK, dV and dLam always are). Given gradients may not require one."""
     if _elsewhere(q, stream):
         with _on(q.device, stream):
             return diff_backward(q, k, v, lam, o, o2, lse, do, causal, scale, dq, dk, dv, dlam, workspace, None,

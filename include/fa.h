@@ -308,7 +308,13 @@ size_t fa_bwd_workspace_size_ex(int B, int H, int Sq, int Sk, int D, int determi
    others are FA_ERR_UNSUPPORTED. dtype, scale, causal mask (bottom-right
    aligned), alignment, ownership, asynchrony and errors as for fa_fwd_ex;
    2 * B * H * Sq (rounded up to 128) below 2^31. The backward holds P_1 - lambda
-   P_2 in the call's type: with fp16, |lambda| has to stay below 65504. */
+   P_2 in the call's type: with fp16, |lambda| has to stay below 65504.
+   Precision: P_c (forward; not in calls of few query rows), P_1 - lambda P_2 and
+   the score gradients (backward) are rounded to the call's type once, as operands
+   of the tensor cores; dlambda is -dO . O_2 of the rounded O_2, so an FA_LAMBDA_FP32
+   one has the call's type's precision too. All sums are fp32.
+   A NaN score makes the rows that see it NaN: o, the map's lse, and the gradients
+   that depend on them. */
 
 /* lambda: one value per (batch, query row, head), or one for all of an axis
    whose extent is 1 (its stride is then not read). dtype: FA_LAMBDA_FP32, or
